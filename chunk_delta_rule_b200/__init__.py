@@ -1,4 +1,5 @@
-"""Comba chunk-wise forward, its backward and the decode step on B200 (sm_100a).
+"""Comba chunk-wise forward, its backward and the decode step on B200 (sm_100a), with the
+short convolution, selective scan and norms of a token-mixer block around them.
 
 Thin ctypes binding over the C ABI in ``include/comba.h``: it checks tensor
 placement, dtypes and contiguity, allocates outputs with PyTorch when the
@@ -21,7 +22,8 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["chunk_fwd", "chunk_bwd", "state_compose", "chunk_fwd_transition", "chunk_fwd_gated", "chunk_fwd_host", "chunk_fwd_varlen", "chunk_fwd_noalloc",
-           "recurrent_step",
+           "recurrent_step", "short_conv", "short_conv_bwd", "short_conv_step", "selective_scan", "selective_scan_bwd",
+           "selective_scan_step", "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd",
            "get_last_error", "CombaError", "library", "library_path", "EXPORTS", "status_string"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +36,13 @@ EXPORTS = ("comba_chunk_fwd", "comba_chunk_fwd_f32", "comba_chunk_fwd_varlen",
            "comba_chunk_fwd_host", "comba_chunk_fwd_host_workspace_size", "comba_chunk_fwd_gated",
            "comba_chunk_bwd", "comba_chunk_bwd_workspace_size", "comba_state_compose",
            "comba_chunk_fwd_transition", "comba_chunk_fwd_stall_test", "comba_chunk_bwd_stall_test",
-           "comba_recurrent_step", "comba_recurrent_step_grouped", "comba_get_last_error",
+           "comba_recurrent_step", "comba_recurrent_step_grouped",
+           "comba_short_conv_fwd", "comba_short_conv_bwd", "comba_short_conv_bwd_workspace_size",
+           "comba_short_conv_step", "comba_selective_scan_fwd", "comba_selective_scan_bwd",
+           "comba_selective_scan_bwd_workspace_size", "comba_selective_scan_step",
+           "comba_gated_norm_fwd", "comba_gated_norm_bwd", "comba_gated_norm_bwd_workspace_size",
+           "comba_residual_norm_fwd", "comba_residual_norm_bwd", "comba_residual_norm_bwd_workspace_size",
+           "comba_get_last_error",
            "comba_get_last_error_stream", "comba_status_string", "comba_version")
 
 
@@ -80,6 +88,24 @@ def library():
                                                         vp])
             lib.comba_chunk_bwd_workspace_size.restype = ctypes.c_size_t
             lib.comba_recurrent_step_grouped.argtypes = [vp] * 8 + [i] * 5 + [vp]
+            ll, f, sz = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+            for name, sig, res in (
+                    ("comba_short_conv_fwd", [vp] * 7 + [i] * 6 + [vp], i),
+                    ("comba_short_conv_bwd", [vp] * 11 + [i] * 6 + [vp, sz, vp], i),
+                    ("comba_short_conv_bwd_workspace_size", [i] * 5, sz),
+                    ("comba_short_conv_step", [vp] * 5 + [i] * 5 + [vp], i),
+                    ("comba_selective_scan_fwd", [vp] * 12 + [i] * 6 + [vp], i),
+                    ("comba_selective_scan_bwd", [vp] * 21 + [i] * 6 + [vp, sz, vp], i),
+                    ("comba_selective_scan_bwd_workspace_size", [i] * 6, sz),
+                    ("comba_selective_scan_step", [vp] * 10 + [i] * 5 + [vp], i),
+                    ("comba_gated_norm_fwd", [vp] * 4 + [ll, i, f, i, vp], i),
+                    ("comba_gated_norm_bwd", [vp] * 7 + [ll, i, f, i, vp, sz, vp], i),
+                    ("comba_gated_norm_bwd_workspace_size", [ll, i], sz),
+                    ("comba_residual_norm_fwd", [vp] * 7 + [ll, i, f, i, i, vp], i),
+                    ("comba_residual_norm_bwd", [vp] * 12 + [ll, i, f, i, i, vp, sz, vp], i),
+                    ("comba_residual_norm_bwd_workspace_size", [ll, i], sz)):
+                fn = getattr(lib, name)
+                fn.argtypes, fn.restype = sig, res
             for fn in (lib.comba_chunk_fwd, lib.comba_chunk_fwd_f32, lib.comba_chunk_fwd_ws,
                        lib.comba_chunk_fwd_noalloc, lib.comba_chunk_fwd_varlen,
                        lib.comba_recurrent_step_grouped, lib.comba_chunk_fwd_host,
@@ -530,3 +556,8 @@ def get_last_error(device=None, stream=None) -> int:
         if stream is None:
             return int(library().comba_get_last_error())
         return int(library().comba_get_last_error_stream(_stream_handle(dev, stream)))
+
+
+from .block_ops import (  # noqa: E402  (uses this module's checks and library handle)
+    gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd, selective_scan, selective_scan_bwd,
+    selective_scan_step, short_conv, short_conv_bwd, short_conv_step)

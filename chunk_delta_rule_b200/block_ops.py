@@ -1,0 +1,364 @@
+"""The operators around and beside the Comba recurrence: short causal convolution,
+selective scan, gated norm and residual norm, each with its backward and, where a model
+decodes with it, its single-token form.
+
+As in the package's other functions, these check tensors, allocate what the caller does
+not pass, and call the C ABI (``include/comba.h``, which states every formula).  Token
+tensors are [B, T, C], or packed [total_T, C] with ``cu_seqlens`` (int32 [N + 1] on the
+device).  Workspaces come from PyTorch's allocator, one per call, so calls on several
+streams and captured graphs do not share them.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+import chunk_delta_rule_b200 as _cdr
+
+__all__ = ["short_conv", "short_conv_bwd", "short_conv_step", "selective_scan", "selective_scan_bwd",
+           "selective_scan_step", "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd"]
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _tensor(t, name: str, dtype, shape, device, optional: bool = False) -> None:
+    if t is None and optional:
+        return
+    _cdr._check(t, name, dtype, shape)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+
+
+def _element(t, name: str) -> torch.dtype:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be bf16 or fp32 (got {t.dtype})")
+    return t.dtype
+
+
+class _Call:
+    """One call of the library: its buffers, of which those allocated here are kept for
+    the caller's stream, and the device and stream it runs on."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.made = device, stream, []
+
+    def new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        self.made.append(t)
+        return t
+
+    def workspace(self, nbytes: int, given: Optional[torch.Tensor]):
+        if given is None:
+            return self.new((max(int(nbytes), 16),), torch.uint8)
+        if given.dtype != torch.uint8 or given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        return given
+
+    def __call__(self, name: str, *args) -> None:
+        lib = _cdr.library()
+        args = [_cdr._ptr(a) if a is None or isinstance(a, torch.Tensor) else a for a in args]
+        with torch.cuda.device(self.device):
+            st = getattr(lib, name)(*args, _cdr._stream_handle(self.device, self.stream))
+            for t in self.made:
+                _cdr._keep_for_stream(t, self.device, self.stream)
+        if st != 0:
+            raise _cdr.CombaError(st, name)
+
+
+def _tokens(x, cu_seqlens, name: str = "x"):
+    """(leading shape, N, T, C) of a token tensor: N sequences of T tokens, or T packed."""
+    _element(x, name)
+    if cu_seqlens is None:
+        if x.dim() != 3:
+            raise ValueError(f"{name} must be [B, T, C]")
+        return tuple(x.shape[:2]), x.shape[0], x.shape[1], x.shape[2]
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [total_T, C] with cu_seqlens")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [N + 1]")
+    return (x.shape[0],), cu_seqlens.numel() - 1, x.shape[0], x.shape[1]
+
+
+def _filter(weight, C: int, dev):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    W = weight.shape[1]
+    _tensor(weight, "weight", torch.float32, (C, W), dev)
+    return W
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+               silu: bool = True, out: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+               return_state: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """comba_short_conv_fwd: causal convolution of W (2, 3 or 4) taps per channel, with
+    SiLU unless ``silu`` is False.  x [B,T,C] or packed [total_T,C], bf16 or fp32; weight
+    [C,W], bias [C] or None fp32; initial_state [N,W-1,C] (the inputs before each
+    sequence, oldest first) or None.  Returns (out like x, final_state [N,W-1,C] or None)."""
+    lead, N, T, C = _tokens(x, cu_seqlens)
+    dt, dev = x.dtype, x.device
+    _tensor(x, "x", dt, (*lead, C), None)
+    W = _filter(weight, C, dev)
+    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new((*lead, C), dt)
+    _tensor(out, "out", dt, (*lead, C), dev)
+    if final_state is None and return_state:
+        final_state = call.new((N, W - 1, C), dt)
+    _tensor(final_state, "final_state", dt, (N, W - 1, C), dev, True)
+    call("comba_short_conv_fwd", x, weight, bias, initial_state, out, final_state, cu_seqlens, N, T, C, W, int(silu),
+         _DTYPE[dt])
+    return out, final_state
+
+
+def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, silu: bool = True,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """comba_short_conv_bwd: gradients of <dout, out> + <dfinal_state, final_state> of
+    short_conv.  Returns a dict of dx (like x), dweight, dbias (None without bias) in fp32
+    and dinitial_state (None without initial_state).  ``workspace``: a uint8 device tensor
+    of at least comba_short_conv_bwd_workspace_size bytes, for this call alone."""
+    lead, N, T, C = _tokens(x, cu_seqlens)
+    dt, dev = x.dtype, x.device
+    _tensor(x, "x", dt, (*lead, C), None)
+    W = _filter(weight, C, dev)
+    _tensor(dout, "dout", dt, (*lead, C), dev)
+    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
+    _tensor(dfinal_state, "dfinal_state", dt, (N, W - 1, C), dev, True)
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
+    call = _Call(dev, stream)
+    g = {"dx": call.new((*lead, C), dt), "dweight": call.new((C, W), torch.float32),
+         "dbias": None if bias is None else call.new((C,), torch.float32),
+         "dinitial_state": None if initial_state is None else call.new((N, W - 1, C), dt)}
+    need = _cdr.library().comba_short_conv_bwd_workspace_size(N, T, C, W, int(cu_seqlens is not None))
+    ws = call.workspace(need, workspace)
+    call("comba_short_conv_bwd", x, weight, bias, initial_state, dout, dfinal_state, g["dx"], g["dweight"], g["dbias"],
+         g["dinitial_state"], cu_seqlens, N, T, C, W, int(silu), _DTYPE[dt], ws, ws.numel())
+    return g
+
+
+def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    silu: bool = True, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """comba_short_conv_step: one token, x [B,C]; ``state`` [B,W-1,C] moves on in place.
+    Returns out [B,C]."""
+    dt = _element(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    B, C = x.shape
+    dev = x.device
+    _tensor(x, "x", dt, (B, C), None)
+    W = _filter(weight, C, dev)
+    _tensor(state, "state", dt, (B, W - 1, C), dev)
+    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new((B, C), dt)
+    _tensor(out, "out", dt, (B, C), dev)
+    call("comba_short_conv_step", x, weight, bias, state, out, B, C, W, int(silu), _DTYPE[dt])
+    return out
+
+
+def _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z):
+    """(groups, states) of a scan whose token tensors have the leading shape ``lead``."""
+    et, dev = x.dtype, x.device
+    _tensor(x, "x", et, (*lead, C), None)
+    _tensor(dt, "dt", et, (*lead, C), dev)
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
+        raise ValueError("Bm must be [..., G, N]")
+    G, N = Bm.shape[-2:]
+    _tensor(A_log, "A_log", torch.float32, (C, N), dev)
+    _tensor(Bm, "Bm", et, (*lead, G, N), dev)
+    _tensor(Cm, "Cm", et, (*lead, G, N), dev)
+    _tensor(D, "D", torch.float32, (C,), dev, True)
+    _tensor(dt_bias, "dt_bias", torch.float32, (C,), dev, True)
+    _tensor(z, "z", et, (*lead, C), dev, True)
+    return G, N
+
+
+def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                   D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   h_final: Optional[torch.Tensor] = None, return_state: bool = True,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """comba_selective_scan_fwd: h_t = exp(delta A) h_{t-1} + delta x_t B_t, out_t =
+    (sum_n h_t C_t + D x_t) silu(z_t), with delta = softplus(dt + dt_bias) and A =
+    -exp(A_log).  x, dt, z [B,T,C] or packed [total_T,C], bf16 or fp32; Bm, Cm [...,G,N]
+    of the same type (G dividing C; N 4 .. 128, a power of two); A_log [C,N], D and
+    dt_bias [C] (or None), h0 [nseq,C,N] (or None) fp32.  Returns (out like x, h_final
+    [nseq,C,N] fp32 or None).  ``h_final`` may be passed as ``h0`` itself."""
+    lead, nseq, T, C = _tokens(x, cu_seqlens)
+    G, N = _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
+    et, dev = x.dtype, x.device
+    _tensor(h0, "h0", torch.float32, (nseq, C, N), dev, True)
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new((*lead, C), et)
+    _tensor(out, "out", et, (*lead, C), dev)
+    if h_final is None and return_state:
+        h_final = call.new((nseq, C, N), torch.float32)
+    _tensor(h_final, "h_final", torch.float32, (nseq, C, N), dev, True)
+    call("comba_selective_scan_fwd", x, dt, A_log, Bm, Cm, D, dt_bias, z, h0, out, h_final, cu_seqlens, nseq, T, C, G, N,
+         _DTYPE[et])
+    return out, h_final
+
+
+def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                       dout: torch.Tensor, D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                       z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                       dh_final: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """comba_selective_scan_bwd: gradients of <dout, out> + <dh_final, h_final> of
+    selective_scan.  Returns a dict of dx, ddt, dBm, dCm, dz (of their inputs' type) and
+    dA_log, dD, ddt_bias, dh0 (fp32); dz, dD, ddt_bias and dh0 are None where their input
+    is.  ``workspace``: a uint8 device tensor of at least
+    comba_selective_scan_bwd_workspace_size bytes, for this call alone."""
+    lead, nseq, T, C = _tokens(x, cu_seqlens)
+    G, N = _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
+    et, dev, f32 = x.dtype, x.device, torch.float32
+    _tensor(dout, "dout", et, (*lead, C), dev)
+    _tensor(h0, "h0", f32, (nseq, C, N), dev, True)
+    _tensor(dh_final, "dh_final", f32, (nseq, C, N), dev, True)
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
+    call = _Call(dev, stream)
+    g = {"dx": call.new((*lead, C), et), "ddt": call.new((*lead, C), et), "dA_log": call.new((C, N), f32),
+         "dBm": call.new((*lead, G, N), et), "dCm": call.new((*lead, G, N), et),
+         "dD": None if D is None else call.new((C,), f32),
+         "ddt_bias": None if dt_bias is None else call.new((C,), f32),
+         "dz": None if z is None else call.new((*lead, C), et),
+         "dh0": None if h0 is None else call.new((nseq, C, N), f32)}
+    need = _cdr.library().comba_selective_scan_bwd_workspace_size(nseq, T, C, G, N, int(cu_seqlens is not None))
+    ws = call.workspace(need, workspace)
+    call("comba_selective_scan_bwd", x, dt, A_log, Bm, Cm, D, dt_bias, z, h0, dout, dh_final, g["dx"], g["ddt"], g["dA_log"],
+         g["dBm"], g["dCm"], g["dD"], g["ddt_bias"], g["dz"], g["dh0"], cu_seqlens, nseq, T, C, G, N, _DTYPE[et], ws,
+         ws.numel())
+    return g
+
+
+def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                        h: torch.Tensor, D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """comba_selective_scan_step: one token, x, dt, z [B,C], Bm, Cm [B,G,N]; the state
+    ``h`` [B,C,N] fp32 is updated in place.  Returns out [B,C]."""
+    et = _element(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    B, C = x.shape
+    dev = x.device
+    G, N = _scan_inputs((B,), C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
+    _tensor(h, "h", torch.float32, (B, C, N), dev)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new((B, C), et)
+    _tensor(out, "out", et, (B, C), dev)
+    call("comba_selective_scan_step", x, dt, A_log, Bm, Cm, D, dt_bias, z, h, out, B, C, G, N, _DTYPE[et])
+    return out
+
+
+def _norm_rows(x, name: str = "x"):
+    dt = _element(x, name)
+    if x.dim() < 1:
+        raise ValueError(f"{name} must be [..., D]")
+    D = x.shape[-1]
+    return dt, D, (x.numel() // D if D else 0)
+
+
+def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """comba_gated_norm_fwd: x / sqrt(mean(x^2) + eps) * weight * silu(gate) over the last
+    dimension, e.g. chunk_fwd's out [B,T,H,dv] per head.  x, gate [..., D] bf16 or fp32;
+    weight [D] fp32; D <= 8192.  Returns out like x."""
+    dt, D, rows = _norm_rows(x)
+    dev = x.device
+    _tensor(x, "x", dt, x.shape, None)
+    _tensor(gate, "gate", dt, x.shape, dev)
+    _tensor(weight, "weight", torch.float32, (D,), dev)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new(tuple(x.shape), dt)
+    _tensor(out, "out", dt, x.shape, dev)
+    call("comba_gated_norm_fwd", x, gate, weight, out, rows, D, float(eps), _DTYPE[dt])
+    return out
+
+
+def gated_norm_bwd(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, eps: float = 1e-6,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """comba_gated_norm_bwd: gradients of <dout, out> of gated_norm, as a dict of dx, dgate
+    (like x) and dweight [D] fp32."""
+    dt, D, rows = _norm_rows(x)
+    dev = x.device
+    _tensor(x, "x", dt, x.shape, None)
+    _tensor(gate, "gate", dt, x.shape, dev)
+    _tensor(weight, "weight", torch.float32, (D,), dev)
+    _tensor(dout, "dout", dt, x.shape, dev)
+    call = _Call(dev, stream)
+    g = {"dx": call.new(tuple(x.shape), dt), "dgate": call.new(tuple(x.shape), dt), "dweight": call.new((D,), torch.float32)}
+    ws = call.workspace(_cdr.library().comba_gated_norm_bwd_workspace_size(rows, D), workspace)
+    call("comba_gated_norm_bwd", x, gate, weight, dout, g["dx"], g["dgate"], g["dweight"], rows, D, float(eps), _DTYPE[dt],
+         ws, ws.numel())
+    return g
+
+
+def _residual_inputs(x, stream_t, name, weight, scale, post_weight):
+    dt, D, rows = _norm_rows(x)
+    dev = x.device
+    _tensor(x, "x", dt, x.shape, None)
+    rt = _element(stream_t, name)
+    if rt not in (dt, torch.float32):
+        raise TypeError(f"{name} must be fp32 or of x's dtype (got {rt})")
+    _tensor(stream_t, name, rt, x.shape, dev)
+    _tensor(weight, "weight", torch.float32, (D,), dev)
+    _tensor(scale, "scale", torch.float32, (D,), dev, True)
+    _tensor(post_weight, "post_weight", torch.float32, (D,), dev, True)
+    return dt, rt, D, rows, dev
+
+
+def residual_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                  h: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """comba_residual_norm_fwd: h = residual + scale * u and out = h / sqrt(mean(h^2) + eps)
+    * weight, with u = x, or x's RMS norm times post_weight.  x [..., D] bf16 or fp32;
+    residual of x's dtype or fp32; weight, scale, post_weight [D] fp32 (the last two or
+    None).  Returns (out like x, h like residual); ``h`` may be ``residual`` itself."""
+    dt, rt, D, rows, dev = _residual_inputs(x, residual, "residual", weight, scale, post_weight)
+    call = _Call(dev, stream)
+    if out is None:
+        out = call.new(tuple(x.shape), dt)
+    _tensor(out, "out", dt, x.shape, dev)
+    if h is None:
+        h = call.new(tuple(x.shape), rt)
+    _tensor(h, "h", rt, x.shape, dev)
+    call("comba_residual_norm_fwd", x, residual, weight, scale, post_weight, out, h, rows, D, float(eps), _DTYPE[dt],
+         _DTYPE[rt])
+    return out, h
+
+
+def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                      post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """comba_residual_norm_bwd: gradients of <dy, out> + <dh, h> of residual_norm, from x
+    and the h it returned.  Returns a dict of dx (like x), dresidual (like h), and dweight,
+    dscale, dpost_weight [D] fp32 (the last two None where their input is)."""
+    dt, rt, D, rows, dev = _residual_inputs(x, h, "h", weight, scale, post_weight)
+    _tensor(dy, "dy", dt, x.shape, dev)
+    _tensor(dh, "dh", rt, x.shape, dev, True)
+    call = _Call(dev, stream)
+    f32 = torch.float32
+    g = {"dx": call.new(tuple(x.shape), dt), "dresidual": call.new(tuple(x.shape), rt), "dweight": call.new((D,), f32),
+         "dscale": None if scale is None else call.new((D,), f32),
+         "dpost_weight": None if post_weight is None else call.new((D,), f32)}
+    ws = call.workspace(_cdr.library().comba_residual_norm_bwd_workspace_size(rows, D), workspace)
+    call("comba_residual_norm_bwd", x, h, weight, scale, post_weight, dy, dh, g["dx"], g["dresidual"], g["dweight"],
+         g["dscale"], g["dpost_weight"], rows, D, float(eps), _DTYPE[dt], _DTYPE[rt], ws, ws.numel())
+    return g

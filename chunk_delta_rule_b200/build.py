@@ -44,14 +44,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
-           "-shared", "-cudart", "static", "-I", INCLUDE, "-o", tmp,
-           os.path.join(CSRC, "comba.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    # each .cu is a translation unit of its own; they compile side by side
+    cmds, objs = [], []
+    for cu in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        objs.append(f"{tmp}.{os.path.basename(cu)}.o")
+        cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+               "-I", INCLUDE, "-c", "-o", objs[-1], cu]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), file=sys.stderr)
+        cmds.append(cmd)
+    try:
+        running = [subprocess.Popen(cmd) for cmd in cmds]
+        for cmd, rc in zip(cmds, [p.wait() for p in running]):
+            if rc != 0:
+                raise subprocess.CalledProcessError(rc, cmd)
+        subprocess.check_call([_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIB
 
 

@@ -1,0 +1,202 @@
+// Helpers of the operators around the recurrence (short convolution, selective scan,
+// norms): 8-element vectors of either element type, activations, the sum of partial
+// rows, argument checks, and the status word shared with the rest of the library.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "comba.h"
+
+namespace comba {
+
+// Device address of the current device's status word (see common.cuh); nullptr if the
+// runtime cannot give it.
+int* status_word();
+
+namespace blk {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kVec = 8;          // elements a thread handles at a time on the vector path
+constexpr int kSMs = 148;        // B200; sizes grids only, results do not depend on it
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
+
+// V consecutive elements at p, as floats.  V == 8 needs 16-byte alignment.
+template <int V>
+__device__ __forceinline__ void load_v(const bf16* __restrict__ p, float (&x)[V]) {
+    if constexpr (V == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else if constexpr (V == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xffff0000u);
+        x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = to_f(p[i]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_v(const float* __restrict__ p, float (&x)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 u = reinterpret_cast<const float4*>(p)[i];
+            x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = p[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int V>
+__device__ __forceinline__ void store_v(bf16* __restrict__ p, const float (&x)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                  pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = __float2bfloat16_rn(x[i]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_v(float* __restrict__ p, const float (&x)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = x[i];
+    }
+}
+
+// sigmoid(v) = 1 / (1 + exp(-v)).  The division is exact enough for fp32 outputs; the
+// exponential overflows to inf only where the quotient is 0.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// Where exp(-v) overflows __fdividef's range (its result is 0 for a divisor above 2^126),
+// 0 is the right value, and v * 0 is (minus) zero for finite v.
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+// d silu / dv
+__device__ __forceinline__ float dsilu(float v) {
+    const float s = sigmoid(v);
+    return s * (1.f + v * (1.f - s));
+}
+
+// softplus(v) = log(1 + exp(v)); above 20 it is v to fp32 precision, and -inf gives 0.
+__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(__expf(v)); }
+
+// Sequence bounds on the joint token axis: N uniform sequences of T tokens, or packed
+// ones with device bounds over T tokens in all.  A packed sequence is well formed if its
+// bounds lie in [0, T] in order; others are skipped.
+struct Seqs {
+    const int* cu;      // nullptr: uniform
+    int N;
+    int T;              // tokens per sequence (uniform) or in all (packed)
+    __host__ __device__ long tokens() const { return cu ? (long)T : (long)N * T; }
+    __device__ __forceinline__ bool bounds(int n, long& s, long& e) const {
+        if (!cu) {
+            s = (long)n * T;
+            e = s + T;
+            return true;
+        }
+        s = cu[n];
+        e = cu[n + 1];
+        return s >= 0 && s <= e && e <= T;
+    }
+    // The last sequence that starts at or before token t (0 if none does).  Whatever the
+    // bounds hold, the answer is in [0, N).
+    __device__ __forceinline__ int find(long t) const {
+        if (!cu) return (int)(t / T);
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// out[c] = sum over rows of part[row][c], in double and in a fixed order: 32 columns by 8
+// row lanes a block.
+__global__ void __launch_bounds__(256)
+sum_rows_kernel(const float* __restrict__ part, float* __restrict__ out, long rows, long cols) {
+    __shared__ double s[8][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const long c = (long)blockIdx.x * 32 + lane;
+    double acc = 0.0;
+    if (c < cols)
+        for (long r = w; r < rows; r += 8) acc += (double)part[r * cols + c];
+    s[w][lane] = acc;
+    __syncthreads();
+    if (w == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) acc += s[i][lane];
+        out[c] = (float)acc;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// One tensor argument of an entry point: its bytes, the alignment it needs and whether it
+// may be null.
+struct Arg {
+    const void* p;
+    size_t bytes;
+    size_t align;
+    bool optional;
+};
+
+// Every argument present (unless optional or empty) and aligned; no output overlaps an
+// input or another output.
+template <int NI, int NO>
+inline bool args_ok(const Arg (&ins)[NI], const Arg (&outs)[NO]) {
+    for (const Arg& a : ins)
+        if ((!a.p && !a.optional && a.bytes) || !aligned(a.p, a.align)) return false;
+    for (const Arg& a : outs)
+        if ((!a.p && !a.optional && a.bytes) || !aligned(a.p, a.align)) return false;
+    for (int i = 0; i < NO; ++i) {
+        for (const Arg& a : ins)
+            if (overlap(outs[i].p, outs[i].bytes, a.p, a.bytes)) return false;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return false;
+    }
+    return true;
+}
+
+inline int launched() { return cudaGetLastError() == cudaSuccess ? COMBA_OK : COMBA_ECUDA; }
+inline long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+}  // namespace blk
+}  // namespace comba

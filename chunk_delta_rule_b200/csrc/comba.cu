@@ -705,6 +705,12 @@ int read_clear_status(cudaStream_t s) {
 
 }  // namespace
 
+// The status word's device address, for kernels of the library's other sources.
+int* comba::status_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, comba::g_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+}
+
 extern "C" int comba_get_last_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return COMBA_ECUDA;
     return read_clear_status(nullptr);

@@ -1,4 +1,4 @@
-// Shared device helpers for the Comba kernels (single translation unit: comba.cu).
+// Shared device helpers for the Comba kernels (translation unit comba.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,6 +22,10 @@ inline std::mutex& init_mutex() {
 __device__ int g_status = 0;
 
 __device__ __forceinline__ void latch_status(int code) { atomicCAS(&g_status, 0, code); }
+
+// Its device address, which kernels of the library's other translation units get as an
+// argument; nullptr if the runtime cannot give it.
+int* status_word();
 
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

@@ -1,0 +1,331 @@
+// Selective state space scan: per channel c a diagonal state of N entries, read and
+// written through token-dependent B_t and C_t shared by the channels of a group,
+//
+//   delta = softplus(dt + dt_bias),  a = exp(delta A),  A = -exp(A_log)
+//   h_t = a h_{t-1} + delta x_t B_t,   y_t = sum_n h_t C_t + D x_t,   out_t = y_t silu(z_t)
+//
+// (the discretisation of comba_chunk_fwd_gated, per channel and state entry instead of per
+// head).  A thread holds 4 neighbouring entries of one channel's state in registers and
+// N / 4 neighbouring lanes hold a channel.
+#pragma once
+
+#include "block_common.cuh"
+
+namespace comba {
+namespace scan {
+
+using namespace blk;
+
+constexpr int kThreads = 128;
+constexpr int kSub = 8;          // tokens between two stored states of the backward
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Params {
+    const void *x, *dt, *Bm, *Cm, *z, *dout;
+    const float *A_log, *D, *dt_bias, *h0, *dh_final;
+    void *out, *dx, *ddt, *dz;
+    float *h_final, *dh0;
+    float* ckpt;                 // [slots, C, N]: the state before every kSub-th token of a sequence
+    float* part_bc;              // [channel blocks, tokens, 2, N]
+    double* part_a;              // [sequences, C, N]
+    double* part_d;              // [sequences, 2, C]: dD and ddt_bias
+    Seqs seq;
+    int C, G, N;
+    int* status;
+};
+
+// 2^v for v <= 0 by the hardware's approximation (relative error 2^-22).
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Slot of the stored state of sub-chunk k of sequence n that starts at token s: a sequence
+// of l tokens has ceil(l / kSub) of them, and s / kSub + n leaves room for them before the
+// next sequence's.
+__host__ __device__ inline long ckpt_slot(long s, int n, long k) { return s / kSub + n + k; }
+inline long ckpt_slots(const Seqs& q) { return q.tokens() / kSub + q.N + 1; }
+
+// Where a thread stands: its channel (of group g) and its first state entry.
+template <int LPC>
+struct Place {
+    int c, g, n0;
+    bool on;
+    __device__ __forceinline__ Place(const Params& p) {
+        constexpr int CB = kThreads / LPC;
+        const int cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
+        g = blockIdx.x / bpg;
+        const int i = (blockIdx.x % bpg) * CB + threadIdx.x / LPC;
+        on = i < cpg;
+        c = g * cpg + (on ? i : 0);
+        n0 = (threadIdx.x % LPC) * 4;
+    }
+};
+
+template <int LPC>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < LPC; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// One block per (channel block, sequence), tokens in order.  CKPT: no outputs, but the
+// state before every kSub-th token (the backward's first sweep).
+template <typename T, int LPC, bool CKPT>
+__global__ void __launch_bounds__(kThreads)
+fwd_kernel(const __grid_constant__ Params p) {
+    constexpr int N = LPC * 4;
+    const Place<LPC> at(p);
+    const int n = blockIdx.y;
+    long s, e;
+    if (!p.seq.bounds(n, s, e)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
+        return;
+    }
+    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f};
+    load_v<4>(p.A_log + (long)at.c * N + at.n0, A2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A2[i] = -expf(A2[i]) * kLog2e;
+    const long hrow = ((long)n * p.C + at.c) * N + at.n0;
+    if (p.h0) load_v<4>(p.h0 + hrow, h);
+    const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f;
+    const float D = p.D ? p.D[at.c] : 0.f;
+    const T* x = static_cast<const T*>(p.x) + at.c;
+    const T* dt = static_cast<const T*>(p.dt) + at.c;
+    const T* z = static_cast<const T*>(p.z);
+    const T* Bm = static_cast<const T*>(p.Bm) + (long)at.g * N + at.n0;
+    const T* Cm = static_cast<const T*>(p.Cm) + (long)at.g * N + at.n0;
+#pragma unroll 4
+    for (long t = s; t < e; ++t) {
+        if (CKPT && (t - s) % kSub == 0 && at.on)
+            store_v<4>(p.ckpt + (ckpt_slot(s, n, (t - s) / kSub) * p.C + at.c) * N + at.n0, h);
+        const float xv = to_f(x[t * p.C]);
+        const float delta = softplus(to_f(dt[t * p.C]) + bias);
+        const float u = delta * xv;
+        float b[4], cc[4], y = 0.f;
+        load_v<4>(Bm + t * p.G * N, b);
+        if (!CKPT) load_v<4>(Cm + t * p.G * N, cc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = fmaf(exp2_fast(delta * A2[i]), h[i], u * b[i]);
+            if (!CKPT) y = fmaf(h[i], cc[i], y);
+        }
+        if (!CKPT) {
+            y = lanes_sum<LPC>(y);
+            if (at.n0 == 0 && at.on) {
+                y = fmaf(D, xv, y);
+                if (z) y *= silu(to_f(z[t * p.C + at.c]));
+                static_cast<T*>(p.out)[t * p.C + at.c] = from_f<T>(y);
+            }
+        }
+    }
+    if (!CKPT && p.h_final && at.on) store_v<4>(p.h_final + hrow, h);
+}
+
+// Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state
+// before a sub-chunk, its decays a and decayed states q = a h_{t-1} are formed again and
+// kept in registers (h_t = q + delta x B); then, with g the state's gradient,
+//   dy = dout silu(z),  dz = dout y silu'(z),  g += C dy,
+//   dC = sum_c h dy,  dB = sum_c g delta x,  du = sum_n g B,
+//   ddelta = sum_n g q A + du x,  dA_log = A sum g q delta,
+//   dx = du delta + D dy,  ddt = ddelta sigmoid(dt + dt_bias),  g <- a g.
+// Sums over a channel's entries go over its lanes; dB and dC are summed over the block's
+// channels and leave one row per channel block.
+template <typename T, int LPC>
+__global__ void __launch_bounds__(kThreads)
+bwd_kernel(const __grid_constant__ Params p) {
+    constexpr int N = LPC * 4, WARPS = kThreads / 32;
+    __shared__ float bc[WARPS][kSub][2][N];
+    const Place<LPC> at(p);
+    const int n = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long s, e;
+    if (!p.seq.bounds(n, s, e)) return;   // reported by the first sweep
+    const long tokens = p.seq.tokens();
+    float A2[4], g[4] = {0.f, 0.f, 0.f, 0.f};
+    load_v<4>(p.A_log + (long)at.c * N + at.n0, A2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A2[i] = -expf(A2[i]) * kLog2e;
+    const long hrow = ((long)n * p.C + at.c) * N + at.n0;
+    if (p.dh_final && at.on) load_v<4>(p.dh_final + hrow, g);
+    const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f;
+    const float D = p.D ? p.D[at.c] : 0.f;
+    const T* Bm = static_cast<const T*>(p.Bm) + (long)at.g * N + at.n0;
+    const T* Cm = static_cast<const T*>(p.Cm) + (long)at.g * N + at.n0;
+    double dA[4] = {0.0, 0.0, 0.0, 0.0}, dD = 0.0, dbias = 0.0;
+    for (long k = (e - s + kSub - 1) / kSub - 1; k >= 0; --k) {
+        const long t0 = s + k * kSub;
+        const int len = (int)min((long)kSub, e - t0);
+        float a[kSub][4], q[kSub][4], dl[kSub], xs[kSub], dyv[kSub], zv[kSub], yv[kSub], dov[kSub];
+        float h[4];
+        load_v<4>(p.ckpt + (ckpt_slot(s, n, k) * p.C + at.c) * N + at.n0, h);
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+            const bool live = at.on && j < len;
+            const long o = (t0 + j) * p.C + at.c;
+            xs[j] = live ? to_f(static_cast<const T*>(p.x)[o]) : 0.f;
+            dl[j] = live ? softplus(to_f(static_cast<const T*>(p.dt)[o]) + bias) : 0.f;
+            dov[j] = live ? to_f(static_cast<const T*>(p.dout)[o]) : 0.f;
+            zv[j] = live && p.z ? to_f(static_cast<const T*>(p.z)[o]) : 0.f;
+            dyv[j] = p.z ? dov[j] * silu(zv[j]) : dov[j];
+            const float u = dl[j] * xs[j];
+            float b[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f}, y = 0.f;
+            if (j < len) {
+                load_v<4>(Bm + (t0 + j) * p.G * N, b);
+                load_v<4>(Cm + (t0 + j) * p.G * N, c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[j][i] = exp2_fast(dl[j] * A2[i]);
+                q[j][i] = a[j][i] * h[i];
+                h[i] = fmaf(u, b[i], q[j][i]);
+                y = fmaf(h[i], c[i], y);
+            }
+            yv[j] = lanes_sum<LPC>(y);
+        }
+        float dAk[4] = {0.f, 0.f, 0.f, 0.f}, dDk = 0.f, dbk = 0.f;
+#pragma unroll
+        for (int j = kSub - 1; j >= 0; --j) {
+            const bool live = at.on && j < len;
+            const float u = dl[j] * xs[j];
+            float b[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f}, db[4], dc[4], du = 0.f, dd = 0.f;
+            if (j < len) {
+                load_v<4>(Bm + (t0 + j) * p.G * N, b);
+                load_v<4>(Cm + (t0 + j) * p.G * N, c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float ht = fmaf(u, b[i], q[j][i]);
+                g[i] = fmaf(c[i], dyv[j], g[i]);
+                dc[i] = ht * dyv[j];
+                db[i] = g[i] * u;
+                du = fmaf(g[i], b[i], du);
+                const float gq = g[i] * q[j][i];
+                dd = fmaf(gq, A2[i], dd);
+                dAk[i] = fmaf(gq, dl[j], dAk[i]);
+                g[i] *= a[j][i];
+            }
+            du = lanes_sum<LPC>(du);
+            dd = lanes_sum<LPC>(dd) * (1.f / kLog2e);
+            if (live && at.n0 == 0) {
+                const long o = (t0 + j) * p.C + at.c;
+                const float ddelta = fmaf(du, xs[j], dd);
+                const float dv = ddelta * sigmoid(to_f(static_cast<const T*>(p.dt)[o]) + bias);
+                static_cast<T*>(p.dx)[o] = from_f<T>(fmaf(du, dl[j], D * dyv[j]));
+                static_cast<T*>(p.ddt)[o] = from_f<T>(dv);
+                if (p.dz) static_cast<T*>(p.dz)[o] = from_f<T>(dov[j] * fmaf(D, xs[j], yv[j]) * dsilu(zv[j]));
+                dDk = fmaf(dyv[j], xs[j], dDk);
+                dbk += dv;
+            }
+            // over the warp's channels
+#pragma unroll
+            for (int o = LPC; o < 32; o *= 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+                    dc[i] += __shfl_xor_sync(0xffffffffu, dc[i], o);
+                }
+            if (lane < LPC)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    bc[warp][j][0][at.n0 + i] = db[i];
+                    bc[warp][j][1][at.n0 + i] = dc[i];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dA[i] += (double)dAk[i];
+        dD += (double)dDk;
+        dbias += (double)dbk;
+        __syncthreads();
+        for (int i = threadIdx.x; i < len * 2 * N; i += kThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) v += (&bc[w][0][0][0])[i];
+            p.part_bc[((long)blockIdx.x * tokens + t0) * 2 * N + i] = v;
+        }
+        __syncthreads();
+    }
+    if (!at.on) return;
+    if (p.dh0) store_v<4>(p.dh0 + hrow, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.part_a[hrow + i] = dA[i];
+    if (at.n0 == 0) {
+        p.part_d[((long)n * 2) * p.C + at.c] = dD;
+        p.part_d[((long)n * 2 + 1) * p.C + at.c] = dbias;
+    }
+}
+
+// dB and dC of a (token, group) from the group's channel blocks, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+sum_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC, const Seqs seq, int G, int N, int bpg) {
+    const long tokens = seq.tokens();
+    const long id = (long)blockIdx.x * 256 + threadIdx.x;   // over [tokens, G, 2, N]
+    const int i = (int)(id % (2 * N));
+    const long tg = id / (2 * N);
+    const int g = (int)(tg % G);
+    const long t = tg / G;
+    if (t >= tokens) return;
+    if (seq.cu) {   // tokens that no sequence covers have no partial sums and keep what they hold
+        long s, e;
+        if (!seq.bounds(seq.find(t), s, e) || t < s || t >= e) return;
+    }
+    float v = 0.f;
+    for (int b = 0; b < bpg; ++b) v += part[(((long)g * bpg + b) * tokens + t) * 2 * N + i];
+    T* out = i < N ? dB : dC;
+    out[(t * G + g) * N + (i < N ? i : i - N)] = from_f<T>(v);
+}
+
+// dA_log, dD and ddt_bias from the sequences' sums, in a fixed order.
+__global__ void __launch_bounds__(256)
+sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ part_d, const float* __restrict__ A_log,
+                  float* __restrict__ dA_log, float* __restrict__ dD, float* __restrict__ dbias, const Seqs seq, int C, int N) {
+    const long id = (long)blockIdx.x * 256 + threadIdx.x, CN = (long)C * N;
+    if (id >= CN + 2 * C) return;
+    const long i = id < CN ? id : id - CN;
+    const double* part = id < CN ? part_a : part_d;
+    const long cols = id < CN ? CN : 2 * C;
+    double v = 0.0;
+    for (int n = 0; n < seq.N; ++n) {
+        long s, e;
+        if (seq.bounds(n, s, e)) v += part[(long)n * cols + i];
+    }
+    if (id < CN) dA_log[i] = (float)(v * -(double)expf(A_log[i]));
+    else if (i < C) { if (dD) dD[i] = (float)v; }
+    else if (dbias) dbias[i - C] = (float)v;
+}
+
+// One token: the state h [B, C, N] is read and written once.
+template <typename T, int LPC>
+__global__ void __launch_bounds__(kThreads)
+step_kernel(const __grid_constant__ Params p) {
+    constexpr int N = LPC * 4;
+    const Place<LPC> at(p);
+    const int n = blockIdx.y;
+    float* hp = p.h_final + ((long)n * p.C + at.c) * N + at.n0;
+    float h[4], A[4], b[4], c[4];
+    load_v<4>(hp, h);
+    load_v<4>(p.A_log + (long)at.c * N + at.n0, A);
+    load_v<4>(static_cast<const T*>(p.Bm) + ((long)n * p.G + at.g) * N + at.n0, b);
+    load_v<4>(static_cast<const T*>(p.Cm) + ((long)n * p.G + at.g) * N + at.n0, c);
+    const long o = (long)n * p.C + at.c;
+    const float xv = to_f(static_cast<const T*>(p.x)[o]);
+    const float delta = softplus(to_f(static_cast<const T*>(p.dt)[o]) + (p.dt_bias ? p.dt_bias[at.c] : 0.f));
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = fmaf(exp2_fast(delta * (-expf(A[i]) * kLog2e)), h[i], delta * xv * b[i]);
+        y = fmaf(h[i], c[i], y);
+    }
+    y = lanes_sum<LPC>(y);
+    if (!at.on) return;
+    store_v<4>(hp, h);
+    if (at.n0 == 0) {
+        if (p.D) y = fmaf(p.D[at.c], xv, y);
+        if (p.z) y *= silu(to_f(static_cast<const T*>(p.z)[o]));
+        static_cast<T*>(p.out)[o] = from_f<T>(y);
+    }
+}
+
+}  // namespace scan
+}  // namespace comba

@@ -1,0 +1,310 @@
+// Short causal convolution over tokens, one filter per channel (the convolution in front
+// of a recurrent mixer's projections):
+//
+//   pre_t = bias + sum_{j < W} w_j x_{t-W+1+j},   out_t = silu(pre_t) or pre_t
+//
+// with the W-1 inputs before a sequence's first token taken from its carried state.  Every
+// token is read and written once, so the kernels are bound by HBM bandwidth: a thread
+// keeps the filter and the last W-1 inputs of 8 neighbouring channels in registers and
+// walks a tile of tokens.
+#pragma once
+
+#include "block_common.cuh"
+
+namespace comba {
+namespace conv {
+
+using namespace blk;
+
+constexpr int kThreads = 128;
+
+struct Params {
+    const float *weight, *bias;     // [C, W], [C] or null
+    const void *x, *init;           // [tokens, C], [N, W-1, C] or null
+    void *out, *fin;                // [tokens, C], [N, W-1, C] or null
+    const void *dout, *dfin;        // backward: cotangents
+    void *dx, *dinit;
+    float* part;                    // [tiles, W+1, C] partial sums of dweight and dbias
+    Seqs seq;
+    int C;
+    int L;                          // tokens in a tile
+    int* status;
+};
+
+template <int W, int V>
+__device__ __forceinline__ void load_filter(const Params& p, int c, float (&w)[W][V], float (&b)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = p.weight[(long)(c + i) * W + j];
+        b[i] = p.bias ? p.bias[c + i] : 0.f;
+    }
+}
+
+// Input of sequence [s, ..) at token t, which may lie up to W-1 before s: there it is the
+// carried state of sequence n (zero without one).
+template <typename T, int W, int V>
+__device__ __forceinline__ void load_x(const Params& p, int n, long s, long t, int c, float (&x)[V]) {
+    if (t >= s) {
+        load_v<V>(static_cast<const T*>(p.x) + t * p.C + c, x);
+    } else if (p.init) {
+        load_v<V>(static_cast<const T*>(p.init) + ((long)n * (W - 1) + (t - s + W - 1)) * p.C + c, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 0.f;
+    }
+}
+
+// One thread per (tile of tokens, V channels), then one per (sequence, state row, V
+// channels) for the final states and the check of the bounds.
+template <typename T, int W, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads)
+fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
+    const long id = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int cv = p.C / V;
+    const long row = id / cv;
+    const int c = (int)(id - row * cv) * V;
+    if (row >= tiles) {
+        const long q = row - tiles;
+        const int n = (int)(q / (W - 1)), m = (int)(q % (W - 1));
+        long s, e;
+        if (!p.seq.bounds(n, s, e)) {
+            atomicCAS(p.status, 0, COMBA_EINVAL);
+            return;
+        }
+        if (p.fin) {
+            float x[V];
+            load_x<T, W, V>(p, n, s, e - (W - 1) + m, c, x);
+            store_v<V>(static_cast<T*>(p.fin) + ((long)n * (W - 1) + m) * p.C + c, x);
+        }
+        return;
+    }
+    const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
+    float w[W][V], b[V];
+    load_filter<W, V>(p, c, w, b);
+    long t = t0;
+    for (int n = p.seq.find(t0); n < p.seq.N && t < t1; ++n) {
+        long s, e;
+        if (!p.seq.bounds(n, s, e) || e <= t) continue;
+        if (s >= t1) break;
+        t = max(t, s);
+        const long stop = min(e, t1);
+        float h[W][V];   // inputs t-W+1 .. t
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) load_x<T, W, V>(p, n, s, t - (W - 1) + j, c, h[j]);
+        const T* xp = static_cast<const T*>(p.x) + t * p.C + c;
+        T* op = static_cast<T*>(p.out) + t * p.C + c;
+#pragma unroll 4
+        for (; t < stop; ++t, xp += p.C, op += p.C) {
+            load_v<V>(xp, h[W - 1]);
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                y[i] = b[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], h[j][i], y[i]);
+                if (SILU) y[i] = silu(y[i]);
+            }
+            store_v<V>(op, y);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
+        }
+    }
+}
+
+// Backward of one tile.  With dpre_t = dout_t silu'(pre_t) (pre recomputed),
+//   dx_t = sum_j w_j dpre_{t+W-1-j} (+ the final state's cotangent),
+//   dw_j = sum_t dpre_t x_{t-W+1+j},   dbias = sum_t dpre_t.
+// A thread walks its tokens and W-1 more of the same sequence, whose dpre it forms again
+// for the tile's last dx; the sums take the tile's own tokens only and go to `part`.
+// dpre of one token: its input is h[W-1], the W-1 before it h[0 .. W-2].
+template <typename T, int W, int V, bool SILU>
+__device__ __forceinline__ void dpre_of(const Params& p, long t, int c, const float (&w)[W][V], const float (&b)[V],
+                                        const float (&h)[W][V], float (&d)[V]) {
+    load_v<V>(static_cast<const T*>(p.dout) + t * p.C + c, d);
+    if (SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float y = b[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) y = fmaf(w[j][i], h[j][i], y);
+            d[i] *= dsilu(y);
+        }
+    }
+}
+
+template <typename T, int W, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads)
+bwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
+    const long id = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int cv = p.C / V;
+    const long row = id / cv;
+    const int c = (int)(id - row * cv) * V;
+    float w[W][V], b[V];
+    load_filter<W, V>(p, c, w, b);
+    if (row >= tiles) {
+        // cotangent of the initial state's row m, the input W-1-m before the first token
+        const long q = row - tiles;
+        const int n = (int)(q / (W - 1)), m = (int)(q % (W - 1));
+        long s, e;
+        if (!p.seq.bounds(n, s, e)) {
+            atomicCAS(p.status, 0, COMBA_EINVAL);
+            return;
+        }
+        if (!p.dinit) return;
+        float g[V];
+        const long at = m - (e - s);   // its row of the final state, of a sequence shorter than that
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = 0.f;
+        if (p.dfin && at >= 0) load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + at) * p.C + c, g);
+        for (int k = 0; k <= m && s + k < e; ++k) {   // token s + k reads it through tap m - k
+            float h[W][V], d[V];
+#pragma unroll
+            for (int j = 0; j < W; ++j) load_x<T, W, V>(p, n, s, s + k - (W - 1) + j, c, h[j]);
+            dpre_of<T, W, V, SILU>(p, s + k, c, w, b, h, d);
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (j == m - k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[i] = fmaf(w[j][i], d[i], g[i]);
+        }
+        store_v<V>(static_cast<T*>(p.dinit) + ((long)n * (W - 1) + m) * p.C + c, g);
+        return;
+    }
+    const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    }
+    long t = t0;
+    for (int n = p.seq.find(t0); n < p.seq.N && t < t1; ++n) {
+        long s, e;
+        if (!p.seq.bounds(n, s, e) || e <= t) continue;
+        if (s >= t1) break;
+        t = max(t, s);
+        const long from = t, stop = min(e, t1);
+        float h[W][V];   // inputs t-W+1 .. t
+        float g[W][V];   // dx of tokens t-W+1 .. t, complete in g[0] once token t is in
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            load_x<T, W, V>(p, n, s, t - (W - 1) + j, c, h[j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[j][i] = 0.f;
+        }
+#pragma unroll 2
+        for (; t < stop + W - 1; ++t) {
+            float d[V];
+            if (t < e) {
+                load_v<V>(static_cast<const T*>(p.x) + t * p.C + c, h[W - 1]);
+                dpre_of<T, W, V, SILU>(p, t, c, w, b, h, d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] = h[W - 1][i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                g[W - 1][i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) g[j][i] = fmaf(w[j][i], d[i], g[j][i]);
+            }
+            if (t < stop) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d[i], h[j][i], dw[j][i]);
+                }
+            }
+            const long o = t - (W - 1);   // the token whose dx is complete
+            if (o >= from) {
+                if (p.dfin && o >= e - (W - 1)) {
+                    float f[V];
+                    load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + (o - (e - (W - 1)))) * p.C + c, f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[0][i] += f[i];
+                }
+                store_v<V>(static_cast<T*>(p.dx) + o * p.C + c, g[0]);
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    h[j][i] = h[j + 1][i];
+                    g[j][i] = g[j + 1][i];
+                }
+        }
+        t = stop;
+    }
+    float* o = p.part + row * (W + 1) * (long)p.C + c;
+#pragma unroll
+    for (int j = 0; j < W; ++j) store_v<V>(o + (long)j * p.C, dw[j]);
+    store_v<V>(o + (long)W * p.C, db);
+}
+
+// dweight [C, W] and dbias [C] from the tiles' partial sums, in double and a fixed order.
+template <int W>
+__global__ void __launch_bounds__(256)
+sum_kernel(const float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias, long tiles, int C) {
+    __shared__ double s[8][33];
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
+    double acc = 0.0;
+    if (c < C)
+        for (long i = r; i < tiles; i += 8) acc += (double)part[(i * (W + 1) + j) * C + c];
+    s[r][lane] = acc;
+    __syncthreads();
+    if (r != 0 || c >= C) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) acc += s[i][lane];
+    if (j < W) dweight[(long)c * W + j] = (float)acc;
+    else if (dbias) dbias[c] = (float)acc;
+}
+
+// One token: out = silu(bias + sum_j w_j [state, x]_j), and the state moves on by x.
+template <typename T, int W, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads)
+step_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+            T* state, T* __restrict__ out, long B, int C) {
+    const long id = (long)blockIdx.x * kThreads + threadIdx.x;
+    const int cv = C / V;
+    const long n = id / cv;
+    if (n >= B) return;
+    const int c = (int)(id - n * cv) * V;
+    Params p{};
+    p.weight = weight;
+    p.bias = bias;
+    float w[W][V], b[V], h[W][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_v<V>(state + (n * (W - 1) + j) * C + c, h[j]);
+    load_v<V>(x + n * C + c, h[W - 1]);
+    load_filter<W, V>(p, c, w, b);
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        y[i] = b[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], h[j][i], y[i]);
+        if (SILU) y[i] = silu(y[i]);
+    }
+    store_v<V>(out + n * C + c, y);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_v<V>(state + (n * (W - 1) + j) * C + c, h[j + 1]);
+}
+
+// Tokens in a tile: long tiles read fewer tokens twice (W-1 a tile) and, in the backward,
+// write fewer partial sums; short ones give enough threads when the tokens are few.
+inline int tile_tokens(long tokens, int cv, int most) {
+    int L = most;
+    while (L > 4 && ceil_div(tokens, L) * cv < (long)kSMs * 512) L /= 2;
+    return L;
+}
+
+}  // namespace conv
+}  // namespace comba

@@ -1,6 +1,6 @@
 /*
  * comba.h -- C ABI of the B200 (sm_100a) Comba chunk-wise forward, its backward
- * and the decode step.
+ * and the decode step, and of the operators around it in a token-mixer block.
  *
  * The method: Comba, "Improving Bilinear RNNs with Closed-loop Control"
  * (PaperWeekly write-up and arXiv abstract 2506.02475).  Comba's recurrent
@@ -364,6 +364,153 @@ int comba_chunk_bwd_stall_test(const void* q, const void* k, const void* v,
  */
 int comba_state_compose(const float* RM, const float* S0, float* S_start, int B, int H, int P,
                         comba_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The operators around and beside the recurrence in a token-mixer block: a short
+ * causal convolution in front of the mixer, a selective (diagonal) state space scan
+ * as another mixer, and the RMS norms after the mixer and between blocks.
+ *
+ * Conventions beyond those at the top:
+ *  - `dtype` (COMBA_BF16 or COMBA_F32) is the element type of every `void*` tensor
+ *    unless stated otherwise; `float*` tensors are fp32.  Arithmetic, states and sums
+ *    are fp32 or wider; bf16 outputs (gradients of bf16 inputs among them) are rounded
+ *    once, to nearest even.
+ *  - Channels are the last, contiguous dimension of token tensors: [B, T, C].  Any C is
+ *    accepted; multiples of 8 with 16-byte aligned pointers use vector accesses.
+ *  - `void*` tensors need the alignment of their element, fp32 ones 4 bytes, unless
+ *    stated otherwise.
+ *  - Sequences: cu_seqlens == NULL means `nseq` sequences of T tokens ([nseq, T, ...]).
+ *    Otherwise cu_seqlens is a DEVICE int32 [nseq + 1] array and token tensors are packed
+ *    [T, ...]: sequence n covers tokens cu_seqlens[n] .. cu_seqlens[n+1]-1 (nondecreasing,
+ *    within 0 .. T).  Tokens that no sequence covers are neither read nor written (their
+ *    gradients neither).  If a sequence's bounds are malformed it is skipped and
+ *    COMBA_EINVAL is latched in the device status word; which tokens are then computed
+ *    is unspecified, but no access leaves the tensors.
+ *  - Every result is the same from run to run (no atomics in sums).
+ *  - Workspaces: DEVICE memory of at least the size the matching function returns,
+ *    16-byte aligned, owned by the caller and in use until `stream` has passed the call;
+ *    calls in flight at the same time need one each.
+ *  - COMBA_EINVAL: a bad size, pointer, alignment, overlap, dtype or workspace;
+ *    COMBA_EUNSUPPORTED: a size beyond a limit stated below.  Nothing is enqueued then.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Short causal convolution, one filter of W taps per channel:
+ *     pre_t = bias + sum_{j < W} weight[c, j] x_{t-W+1+j},    out_t = silu(pre_t)
+ * (pre_t itself when silu == 0).  The W - 1 inputs before a sequence's first token are
+ * its initial_state [nseq, W-1, C], oldest first (NULL: zeros); final_state [nseq, W-1, C]
+ * (NULL: not written) receives the last W - 1 inputs, which continue the sequence in
+ * another call or in comba_short_conv_step.  W in {2, 3, 4}; weight [C, W], bias [C] or
+ * NULL.  final_state must not overlap initial_state.
+ */
+int comba_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                         void* out, void* final_state, const int* cu_seqlens, int nseq, int T, int C, int W,
+                         int silu, int dtype, comba_stream_t stream);
+
+/*
+ * Gradients of <dout, out> + <dfinal_state, final_state> of comba_short_conv_fwd: dx and
+ * dinitial_state [nseq, W-1, C] (NULL: skipped) in the element type, dweight [C, W] and
+ * dbias [C] (NULL: skipped) in fp32.  dfinal_state may be NULL (zero).  `packed` in the
+ * workspace size says whether cu_seqlens is given.
+ */
+size_t comba_short_conv_bwd_workspace_size(int nseq, int T, int C, int W, int packed);
+int comba_short_conv_bwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                         const void* dout, const void* dfinal_state, void* dx, float* dweight, float* dbias,
+                         void* dinitial_state, const int* cu_seqlens, int nseq, int T, int C, int W, int silu,
+                         int dtype, void* workspace, size_t workspace_bytes, comba_stream_t stream);
+
+/*
+ * One token of the convolution for every sequence: x, out [B, C]; state [B, W-1, C] is
+ * read and moved on by x in place.
+ */
+int comba_short_conv_step(const void* x, const float* weight, const float* bias, void* state, void* out, int B,
+                          int C, int W, int silu, int dtype, comba_stream_t stream);
+
+/*
+ * Selective state space scan.  Per channel c and state entry n, with the channels in G
+ * equal groups that share B and C,
+ *     delta_t = softplus(dt_t + dt_bias),   A = -exp(A_log)
+ *     h_t[c, n] = exp(delta_t[c] A[c, n]) h_{t-1}[c, n] + delta_t[c] x_t[c] B_t[g(c), n]
+ *     y_t[c] = sum_n h_t[c, n] C_t[g(c), n] + D[c] x_t[c],     out_t = y_t silu(z_t)
+ * (the discretisation of comba_chunk_fwd_gated, per channel and entry).  dt = -inf makes
+ * a token leave the state as it is.
+ *
+ * x, dt, z, out: token tensors of C channels (z NULL: out = y).  Bm, Cm: [tokens, G, N].
+ * A_log [C, N], D [C] or NULL (zero), dt_bias [C] or NULL (zero), h0 and h_final
+ * [nseq, C, N]: fp32 (h0 NULL: zero; h_final NULL: not written; h_final may be h0 itself,
+ * but overlap it in no other way).  G must divide C; N in {4, 8, 16, 32, 64, 128}.  A_log,
+ * Bm, Cm, h0 and h_final 16-byte aligned.  nseq <= 65535 (COMBA_EUNSUPPORTED above).
+ */
+int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
+                             const float* D, const float* dt_bias, const void* z, const float* h0, void* out,
+                             float* h_final, const int* cu_seqlens, int nseq, int T, int C, int G, int N,
+                             int dtype, comba_stream_t stream);
+
+/*
+ * Gradients of <dout, out> + <dh_final, h_final> of comba_selective_scan_fwd with respect
+ * to every input: dx, ddt, dz, dBm, dCm in the element type, dA_log [C, N], dD [C],
+ * ddt_bias [C] and dh0 [nseq, C, N] in fp32.  dz is given exactly when z is; dD, ddt_bias
+ * and dh0 may be NULL (skipped), dh_final too (zero).  The states are formed again, from
+ * h0; the outputs of the forward are not needed.  dh0 and dh_final 16-byte aligned.
+ */
+size_t comba_selective_scan_bwd_workspace_size(int nseq, int T, int C, int G, int N, int packed);
+int comba_selective_scan_bwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
+                             const float* D, const float* dt_bias, const void* z, const float* h0,
+                             const void* dout, const float* dh_final, void* dx, void* ddt, float* dA_log,
+                             void* dBm, void* dCm, float* dD, float* ddt_bias, void* dz, float* dh0,
+                             const int* cu_seqlens, int nseq, int T, int C, int G, int N, int dtype,
+                             void* workspace, size_t workspace_bytes, comba_stream_t stream);
+
+/*
+ * One token of the scan for every sequence: x, dt, z, out [B, C]; Bm, Cm [B, G, N]; the
+ * state h [B, C, N] fp32 (16-byte aligned) is read and overwritten.  B <= 65535.
+ */
+int comba_selective_scan_step(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
+                              const float* D, const float* dt_bias, const void* z, float* h, void* out, int B,
+                              int C, int G, int N, int dtype, comba_stream_t stream);
+
+/*
+ * RMS norm over rows of D values, times a gate's SiLU (the norm of a mixer's output, per
+ * head when rows are heads):
+ *     out = x / sqrt(mean(x^2) + eps) * weight * silu(gate)
+ * x, gate, out [rows, D]; weight [D]; eps >= 0.  D <= 8192 (COMBA_EUNSUPPORTED above).
+ */
+int comba_gated_norm_fwd(const void* x, const void* gate, const float* weight, void* out, long long rows, int D,
+                         float eps, int dtype, comba_stream_t stream);
+
+/* Gradients of <dout, out>: dx, dgate [rows, D] in the element type, dweight [D] fp32. */
+size_t comba_gated_norm_bwd_workspace_size(long long rows, int D);
+int comba_gated_norm_bwd(const void* x, const void* gate, const float* weight, const void* dout, void* dx,
+                         void* dgate, float* dweight, long long rows, int D, float eps, int dtype,
+                         void* workspace, size_t workspace_bytes, comba_stream_t stream);
+
+/*
+ * A block's output x added onto the residual stream, and the norm of the sum that the
+ * next block reads:
+ *     u = x,  or  x / sqrt(mean(x^2) + eps) * post_weight  when post_weight is given
+ *     h = residual + scale * u        (scale [D], NULL: 1)
+ *     out = h / sqrt(mean(h^2) + eps) * weight
+ * x, out [rows, D] of `dtype`; residual, h [rows, D] of `residual_dtype` (COMBA_F32, or
+ * the same as dtype).  The norm reads h as it is stored.  h may be residual itself (in
+ * place).  D <= 8192 (COMBA_EUNSUPPORTED above).
+ */
+int comba_residual_norm_fwd(const void* x, const void* residual, const float* weight, const float* scale,
+                            const float* post_weight, void* out, void* h, long long rows, int D, float eps,
+                            int dtype, int residual_dtype, comba_stream_t stream);
+
+/*
+ * Gradients of <dy, out> + <dh, h> (dh NULL: zero), from x and the h that the forward
+ * stored: dx of `dtype`, dresidual of `residual_dtype`, dweight, dscale, dpost_weight [D]
+ * fp32 (dscale and dpost_weight NULL: skipped; refused where scale or post_weight is NULL).
+ */
+size_t comba_residual_norm_bwd_workspace_size(long long rows, int D);
+int comba_residual_norm_bwd(const void* x, const void* h, const float* weight, const float* scale,
+                            const float* post_weight, const void* dy, const void* dh, void* dx, void* dresidual,
+                            float* dweight, float* dscale, float* dpost_weight, long long rows, int D, float eps,
+                            int dtype, int residual_dtype, void* workspace, size_t workspace_bytes,
+                            comba_stream_t stream);
 
 /*
  * Reads and clears the current device's status word (synchronises the
