@@ -217,14 +217,14 @@ ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
 template <typename T, int LPC>
 int scan_fwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    scan::fwd_kernel<T, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
+    scan::fwd_kernel<T, 4, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
 }
 
 template <typename T, int LPC>
 int scan_bwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    scan::fwd_kernel<T, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
+    scan::fwd_kernel<T, 4, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
     scan::bwd_kernel<T, LPC><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
 }

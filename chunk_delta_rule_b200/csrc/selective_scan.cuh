@@ -70,57 +70,149 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// One block per (channel block, sequence), tokens in order.  CKPT: no outputs, but the
-// state before every kSub-th token (the backward's first sweep).
-template <typename T, int LPC, bool CKPT>
+// Sums of M values over the M lanes (M a power of two) that differ in lane bits [S, S * M):
+// the lane whose those bits are r ends with the sum of v[r] in v[0].  M - 1 shuffles, each
+// halving the values a lane still holds, instead of M log2 M.
+template <int M, int S>
+__device__ __forceinline__ void transpose_sum(float (&v)[M], int lane) {
+#pragma unroll
+    for (int w = M / 2; w > 0; w /= 2) {
+        const bool up = lane & (w * S);
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w * S);
+        }
+    }
+}
+
+// Tokens of a tile: what a block stages in shared memory at a time.
+__host__ __device__ constexpr int tile_tokens(int lpc) { return lpc == 1 ? 8 : lpc <= 16 ? 16 : 32; }
+
+// One block per (channel block, sequence), tokens in order, a tile at a time.  NP state
+// entries a thread, LPC lanes a channel.
+//
+// A tile passes through three phases.  (1) Each of its (token, channel) pairs has one
+// thread, which forms delta and delta x for all the channel's lanes; B and C become fp32 in
+// shared memory.  (2) The lanes walk the tile's tokens, with only the state's own chain
+// between them, and sum y over a channel's lanes for LPC tokens at a time.  (3) The
+// pair's thread adds D x, applies the gate and stores.  The next tile's loads are in
+// flight during (2).
+// The exponentials bound it (16 a clock and SM), then the issue slots.
+// CKPT: no outputs, but the state before every kSub-th token (the backward's first sweep).
+template <typename T, int NP, int LPC, bool CKPT>
 __global__ void __launch_bounds__(kThreads)
 fwd_kernel(const __grid_constant__ Params p) {
-    constexpr int N = LPC * 4;
-    const Place<LPC> at(p);
-    const int n = blockIdx.y;
+    constexpr int N = NP * LPC, TT = tile_tokens(LPC), CB = kThreads / LPC, EL = TT / LPC;
+    constexpr int QUADS = TT * N / 4;                         // of B, and as many of C
+    constexpr int QP = (2 * QUADS + kThreads - 1) / kThreads;
+    __shared__ float2 du_s[TT][CB];                           // delta, delta x
+    __shared__ __align__(16) float bc_s[2][TT][N];
+    __shared__ float y_s[TT][CB + 8];
+    const int n = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     long s, e;
     if (!p.seq.bounds(n, s, e)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
+        if (blockIdx.x == 0 && tid == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
         return;
     }
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-    load_v<4>(p.A_log + (long)at.c * N + at.n0, A2);
+    const int cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
+    const int g = blockIdx.x / bpg, c0 = (blockIdx.x % bpg) * CB;   // first channel within the group
+    // as a lane of the scan: channel and first state entry
+    const bool on = c0 + tid / LPC < cpg;
+    const int c = g * cpg + (on ? c0 + tid / LPC : 0), n0 = (tid % LPC) * NP;
+    float A2[NP], h[NP];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = -expf(A2[i]) * kLog2e;
-    const long hrow = ((long)n * p.C + at.c) * N + at.n0;
-    if (p.h0) load_v<4>(p.h0 + hrow, h);
-    const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f;
-    const float D = p.D ? p.D[at.c] : 0.f;
-    const T* x = static_cast<const T*>(p.x) + at.c;
-    const T* dt = static_cast<const T*>(p.dt) + at.c;
-    const T* z = static_cast<const T*>(p.z);
-    const T* Bm = static_cast<const T*>(p.Bm) + (long)at.g * N + at.n0;
-    const T* Cm = static_cast<const T*>(p.Cm) + (long)at.g * N + at.n0;
-#pragma unroll 4
-    for (long t = s; t < e; ++t) {
-        if (CKPT && (t - s) % kSub == 0 && at.on)
-            store_v<4>(p.ckpt + (ckpt_slot(s, n, (t - s) / kSub) * p.C + at.c) * N + at.n0, h);
-        const float xv = to_f(x[t * p.C]);
-        const float delta = softplus(to_f(dt[t * p.C]) + bias);
-        const float u = delta * xv;
-        float b[4], cc[4], y = 0.f;
-        load_v<4>(Bm + t * p.G * N, b);
-        if (!CKPT) load_v<4>(Cm + t * p.G * N, cc);
+    for (int i = 0; i < NP; ++i) {
+        A2[i] = -expf(p.A_log[(long)c * N + n0 + i]) * kLog2e;
+        h[i] = p.h0 ? p.h0[((long)n * p.C + c) * N + n0 + i] : 0.f;
+    }
+    // as the thread of (token, channel) pairs: channel pc, tokens pt, pt + LPC, ...
+    const int pi = tid % CB, pt = tid / CB;
+    const bool pon = c0 + pi < cpg;
+    const int pc = g * cpg + (pon ? c0 + pi : 0);
+    const float bias = p.dt_bias ? p.dt_bias[pc] : 0.f;
+    const float D = p.D ? p.D[pc] : 0.f;
+
+    T xr[EL], dr[EL], zr[EL];
+    float br[QP][4];
+    auto fetch = [&](long t0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = fmaf(exp2_fast(delta * A2[i]), h[i], u * b[i]);
-            if (!CKPT) y = fmaf(h[i], cc[i], y);
+        for (int k = 0; k < EL; ++k) {
+            const long t = t0 + pt + k * LPC;
+            const bool ok = pon && t < e;
+            const long o = t * p.C + pc;
+            xr[k] = ok ? static_cast<const T*>(p.x)[o] : from_f<T>(0.f);
+            dr[k] = ok ? static_cast<const T*>(p.dt)[o] : from_f<T>(0.f);
+            if (!CKPT && p.z) zr[k] = ok ? static_cast<const T*>(p.z)[o] : from_f<T>(0.f);
         }
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = tid + k * kThreads, which = q / QUADS, r = q % QUADS;
+            const long t = t0 + r / (N / 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) br[k][i] = 0.f;
+            if (which < (CKPT ? 1 : 2) && t < e)
+                load_v<4>(static_cast<const T*>(which ? p.Cm : p.Bm) + (t * p.G + g) * N + r % (N / 4) * 4, br[k]);
+        }
+    };
+    fetch(s);
+    for (long t0 = s; t0 < e; t0 += TT) {
+        float x[EL], z[EL];
+#pragma unroll
+        for (int k = 0; k < EL; ++k) {
+            const int j = pt + k * LPC;
+            x[k] = to_f(xr[k]);
+            if (!CKPT && p.z) z[k] = to_f(zr[k]);
+            // past the end: delta = 0 leaves the state as it is
+            const float delta = t0 + j < e ? softplus(to_f(dr[k]) + bias) : 0.f;
+            du_s[j][pi] = make_float2(delta, delta * x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = tid + k * kThreads;
+            if (q < 2 * QUADS) store_v<4>(&bc_s[0][0][0] + q * 4, br[k]);
+        }
+        __syncthreads();
+        if (t0 + TT < e) fetch(t0 + TT);
+#pragma unroll
+        for (int j0 = 0; j0 < TT; j0 += LPC) {
+            float y[LPC];
+#pragma unroll
+            for (int jj = 0; jj < LPC; ++jj) {
+                const int j = j0 + jj;
+                if (CKPT && j % kSub == 0 && on && t0 + j < e) {
+                    float* o = p.ckpt + (ckpt_slot(s, n, (t0 - s + j) / kSub) * p.C + c) * N + n0;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) o[i] = h[i];
+                }
+                const float2 du = du_s[j][tid / LPC];
+                y[jj] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    h[i] = fmaf(exp2_fast(du.x * A2[i]), h[i], du.y * bc_s[0][j][n0 + i]);
+                    if (!CKPT) y[jj] = fmaf(h[i], bc_s[1][j][n0 + i], y[jj]);
+                }
+            }
+            if (!CKPT) {
+                transpose_sum<LPC, 1>(y, lane);
+                y_s[j0 + tid % LPC][tid / LPC] = y[0];
+            }
+        }
+        __syncthreads();
         if (!CKPT) {
-            y = lanes_sum<LPC>(y);
-            if (at.n0 == 0 && at.on) {
-                y = fmaf(D, xv, y);
-                if (z) y *= silu(to_f(z[t * p.C + at.c]));
-                static_cast<T*>(p.out)[t * p.C + at.c] = from_f<T>(y);
+#pragma unroll
+            for (int k = 0; k < EL; ++k) {
+                const int j = pt + k * LPC;
+                if (!pon || t0 + j >= e) continue;
+                float y = fmaf(D, x[k], y_s[j][pi]);
+                if (p.z) y *= silu(z[k]);
+                static_cast<T*>(p.out)[(t0 + j) * p.C + pc] = from_f<T>(y);
             }
         }
     }
-    if (!CKPT && p.h_final && at.on) store_v<4>(p.h_final + hrow, h);
+    if (!CKPT && p.h_final && on)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) p.h_final[((long)n * p.C + c) * N + n0 + i] = h[i];
 }
 
 // Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state
