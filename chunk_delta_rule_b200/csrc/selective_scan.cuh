@@ -41,6 +41,57 @@ __device__ __forceinline__ float exp2_fast(float v) {
     return r;
 }
 
+// Pairs of fp32 values in a 64-bit register: one instruction for two products or sums, so
+// that the issue slots do not bound the state's update.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair exp2_pair(Pair v) {
+    float a, b;
+    unpair(v, a, b);
+    return pair(exp2_fast(a), exp2_fast(b));
+}
+// NP / 2 pairs at p (16-byte aligned for NP >= 4).
+template <int NP>
+__device__ __forceinline__ void load_pairs(const float* p, Pair (&v)[NP / 2]) {
+    if constexpr (NP % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) {
+            const ulonglong2 u = reinterpret_cast<const ulonglong2*>(p)[i];
+            v[2 * i] = u.x;
+            v[2 * i + 1] = u.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) v[i] = reinterpret_cast<const Pair*>(p)[i];
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[NP / 2]) {
+    if constexpr (NP % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) reinterpret_cast<ulonglong2*>(p)[i] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) reinterpret_cast<Pair*>(p)[i] = v[i];
+    }
+}
+
 // Slot of the stored state of sub-chunk k of sequence n that starts at token s: a sequence
 // of l tokens has ceil(l / kSub) of them, and s / kSub + n leaves room for them before the
 // next sequence's.
@@ -120,11 +171,13 @@ fwd_kernel(const __grid_constant__ Params p) {
     // as a lane of the scan: channel and first state entry
     const bool on = c0 + tid / LPC < cpg;
     const int c = g * cpg + (on ? c0 + tid / LPC : 0), n0 = (tid % LPC) * NP;
-    float A2[NP], h[NP];
+    const long hrow = ((long)n * p.C + c) * N + n0;
+    Pair A2[NP / 2], h[NP / 2];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        A2[i] = -expf(p.A_log[(long)c * N + n0 + i]) * kLog2e;
-        h[i] = p.h0 ? p.h0[((long)n * p.C + c) * N + n0 + i] : 0.f;
+    for (int i = 0; i < NP / 2; ++i) {
+        const float* a = p.A_log + (long)c * N + n0 + 2 * i;
+        A2[i] = pair(-expf(a[0]) * kLog2e, -expf(a[1]) * kLog2e);
+        h[i] = p.h0 ? pair(p.h0[hrow + 2 * i], p.h0[hrow + 2 * i + 1]) : pair(0.f, 0.f);
     }
     // as the thread of (token, channel) pairs: channel pc, tokens pt, pt + LPC, ...
     const int pi = tid % CB, pt = tid / CB;
@@ -181,16 +234,22 @@ fwd_kernel(const __grid_constant__ Params p) {
             for (int jj = 0; jj < LPC; ++jj) {
                 const int j = j0 + jj;
                 if (CKPT && j % kSub == 0 && on && t0 + j < e) {
-                    float* o = p.ckpt + (ckpt_slot(s, n, (t0 - s + j) / kSub) * p.C + c) * N + n0;
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) o[i] = h[i];
+                    store_pairs<NP>(p.ckpt + (ckpt_slot(s, n, (t0 - s + j) / kSub) * p.C + c) * N + n0, h);
                 }
                 const float2 du = du_s[j][tid / LPC];
-                y[jj] = 0.f;
+                const Pair dl = pair(du.x, du.x), u = pair(du.y, du.y);
+                Pair b[NP / 2], cc[NP / 2], acc;
+                load_pairs<NP>(&bc_s[0][j][n0], b);
+                if (!CKPT) load_pairs<NP>(&bc_s[1][j][n0], cc);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    h[i] = fmaf(exp2_fast(du.x * A2[i]), h[i], du.y * bc_s[0][j][n0 + i]);
-                    if (!CKPT) y[jj] = fmaf(h[i], bc_s[1][j][n0 + i], y[jj]);
+                for (int i = 0; i < NP / 2; ++i) {
+                    h[i] = fma2(exp2_pair(mul2(dl, A2[i])), h[i], mul2(u, b[i]));
+                    if (!CKPT) acc = i == 0 ? mul2(h[i], cc[i]) : fma2(h[i], cc[i], acc);
+                }
+                if (!CKPT) {
+                    float lo, hi;
+                    unpair(acc, lo, hi);
+                    y[jj] = lo + hi;
                 }
             }
             if (!CKPT) {
@@ -210,9 +269,7 @@ fwd_kernel(const __grid_constant__ Params p) {
             }
         }
     }
-    if (!CKPT && p.h_final && on)
-#pragma unroll
-        for (int i = 0; i < NP; ++i) p.h_final[((long)n * p.C + c) * N + n0 + i] = h[i];
+    if (!CKPT && p.h_final && on) store_pairs<NP>(p.h_final + hrow, h);
 }
 
 // Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state
