@@ -192,7 +192,7 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: t
     """comba_selective_scan_fwd: h_t = exp(delta A) h_{t-1} + delta x_t B_t, out_t =
     (sum_n h_t C_t + D x_t) silu(z_t), with delta = softplus(dt + dt_bias) and A =
     -exp(A_log).  x, dt, z [B,T,C] or packed [total_T,C], bf16 or fp32; Bm, Cm [...,G,N]
-    of the same type (G dividing C; N 4 .. 128, a power of two); A_log [C,N], D and
+    of the same type (G dividing C; N 8 .. 128, a power of two); A_log [C,N], D and
     dt_bias [C] (or None), h0 [nseq,C,N] (or None) fp32.  Returns (out like x, h_final
     [nseq,C,N] fp32 or None).  ``h_final`` may be passed as ``h0`` itself."""
     lead, nseq, T, C = _tokens(x, cu_seqlens)

@@ -193,7 +193,16 @@ extern "C" int comba_short_conv_step(const void* x, const float* weight, const f
 // ------------------------------------------------------------------ selective scan
 namespace {
 
-bool states_ok(int N) { return N == 4 || N == 8 || N == 16 || N == 32 || N == 64 || N == 128; }
+bool states_ok(int N) { return N == 8 || N == 16 || N == 32 || N == 64 || N == 128; }
+
+// Whether groups of consecutive channels lie whole and aligned in every token tensor.
+bool scan_vector(int C, int G, int N, int dtype, std::initializer_list<const void*> ptrs) {
+    const int e = scan::group_channels(N / 4);
+    if (C / G % e) return false;
+    for (const void* p : ptrs)
+        if (!aligned(p, e * elt_size(dtype))) return false;
+    return true;
+}
 
 // Channel blocks of one group.
 int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, scan::kThreads / (N / 4)); }
@@ -217,14 +226,16 @@ ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
 template <typename T, int LPC>
 int scan_fwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    scan::fwd_kernel<T, 4, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
+    if (p.vec) scan::fwd_kernel<T, LPC, scan::kOutputs, true><<<grid, scan::kThreads, 0, s>>>(p);
+    else scan::fwd_kernel<T, LPC, scan::kOutputs, false><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
 }
 
 template <typename T, int LPC>
 int scan_bwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    scan::fwd_kernel<T, 4, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
+    if (p.vec) scan::fwd_kernel<T, LPC, scan::kStates, true><<<grid, scan::kThreads, 0, s>>>(p);
+    else scan::fwd_kernel<T, LPC, scan::kStates, false><<<grid, scan::kThreads, 0, s>>>(p);
     scan::bwd_kernel<T, LPC><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
 }
@@ -249,7 +260,7 @@ int scan_sums(const scan::Params& p, void* dB, void* dC, float* dA_log, float* d
 }
 
 #define COMBA_SCAN_LPC(f, T, N, ...)                                                                         \
-    ((N) == 4 ? f<T, 1>(__VA_ARGS__) : (N) == 8 ? f<T, 2>(__VA_ARGS__) : (N) == 16 ? f<T, 4>(__VA_ARGS__)    \
+    ((N) == 8 ? f<T, 2>(__VA_ARGS__) : (N) == 16 ? f<T, 4>(__VA_ARGS__)    \
      : (N) == 32 ? f<T, 8>(__VA_ARGS__) : (N) == 64 ? f<T, 16>(__VA_ARGS__) : f<T, 32>(__VA_ARGS__))
 #define COMBA_SCAN_DISPATCH(f, dtype, N, ...) \
     ((dtype) == COMBA_BF16 ? COMBA_SCAN_LPC(f, bf16, N, __VA_ARGS__) : COMBA_SCAN_LPC(f, float, N, __VA_ARGS__))
@@ -286,6 +297,7 @@ extern "C" int comba_selective_scan_fwd(const void* x, const void* dt, const flo
     p.out = out; p.h_final = h_final;
     p.seq = Seqs{cu_seqlens, nseq, T};
     p.C = C; p.G = G; p.N = N;
+    p.vec = scan_vector(C, G, N, dtype, {x, dt, z, out});
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     return COMBA_SCAN_DISPATCH(scan_fwd, dtype, N, p, reinterpret_cast<cudaStream_t>(stream));
@@ -323,6 +335,7 @@ extern "C" int comba_selective_scan_bwd(const void* x, const void* dt, const flo
     p.dout = dout; p.dh_final = dh_final; p.dx = dx; p.ddt = ddt; p.dz = dz; p.dh0 = dh0;
     p.seq = Seqs{cu_seqlens, nseq, T};
     p.C = C; p.G = G; p.N = N;
+    p.vec = scan_vector(C, G, N, dtype, {x, dt, z, dout, dx, ddt, dz});
     char* w = static_cast<char*>(workspace);
     const ScanWs ws = scan_ws(p.seq, C, G, N);
     p.ckpt = reinterpret_cast<float*>(w + ws.ckpt);

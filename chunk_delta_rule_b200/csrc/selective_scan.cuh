@@ -17,6 +17,7 @@ namespace scan {
 using namespace blk;
 
 constexpr int kThreads = 128;
+constexpr int kBatch = 4;        // tokens whose operands a lane holds at a time
 constexpr int kSub = 8;          // tokens between two stored states of the backward
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -31,6 +32,7 @@ struct Params {
     double* part_d;              // [sequences, 2, C]: dD and ddt_bias
     Seqs seq;
     int C, G, N;
+    bool vec;                    // groups of channels lie whole and aligned (see load_group)
     int* status;
 };
 
@@ -98,22 +100,6 @@ __device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[NP / 2]) {
 __host__ __device__ inline long ckpt_slot(long s, int n, long k) { return s / kSub + n + k; }
 inline long ckpt_slots(const Seqs& q) { return q.tokens() / kSub + q.N + 1; }
 
-// Where a thread stands: its channel (of group g) and its first state entry.
-template <int LPC>
-struct Place {
-    int c, g, n0;
-    bool on;
-    __device__ __forceinline__ Place(const Params& p) {
-        constexpr int CB = kThreads / LPC;
-        const int cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
-        g = blockIdx.x / bpg;
-        const int i = (blockIdx.x % bpg) * CB + threadIdx.x / LPC;
-        on = i < cpg;
-        c = g * cpg + (on ? i : 0);
-        n0 = (threadIdx.x % LPC) * 4;
-    }
-};
-
 template <int LPC>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -121,155 +107,239 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// Sums of M values over the M lanes (M a power of two) that differ in lane bits [S, S * M):
-// the lane whose those bits are r ends with the sum of v[r] in v[0].  M - 1 shuffles, each
-// halving the values a lane still holds, instead of M log2 M.
-template <int M, int S>
-__device__ __forceinline__ void transpose_sum(float (&v)[M], int lane) {
+// Tokens of a tile, which a block stages in shared memory at a time, and the consecutive
+// channels of one token that a thread prepares: every thread has one such group a tile.
+__host__ __device__ constexpr int tile_tokens(int lpc) { return lpc < 8 ? 4 * lpc : 32; }
+__host__ __device__ constexpr int group_channels(int lpc) { return tile_tokens(lpc) / lpc; }
+
+// E consecutive elements.  VEC: as one access (all such groups are whole and aligned), else
+// one by one, those past the first `count` from the first one's place.  Loads carry no
+// condition, so that they stay in flight until their values are needed; what lies outside
+// the tile is masked there.
+template <typename T, int E>
+struct alignas(E * sizeof(T)) Group {
+    T v[E];
+};
+template <bool VEC, typename T, int E>
+__device__ __forceinline__ Group<T, E> load_group(const void* base, long o, int count) {
+    const T* p = static_cast<const T*>(base) + o;
+    if constexpr (VEC) {
+        return *reinterpret_cast<const Group<T, E>*>(p);
+    } else {
+        Group<T, E> r;
 #pragma unroll
-    for (int w = M / 2; w > 0; w /= 2) {
-        const bool up = lane & (w * S);
+        for (int i = 0; i < E; ++i) r.v[i] = p[i < count ? i : 0];
+        return r;
+    }
+}
+template <bool VEC, typename T, int E>
+__device__ __forceinline__ void store_group(void* base, long o, const float (&f)[E], int count) {
+    T* p = static_cast<T*>(base) + o;
+    Group<T, E> r;
 #pragma unroll
-        for (int i = 0; i < w; ++i) {
-            const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w * S);
-        }
+    for (int i = 0; i < E; ++i) r.v[i] = from_f<T>(f[i]);
+    if constexpr (VEC) {
+        *reinterpret_cast<Group<T, E>*>(p) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (i < count) p[i] = r.v[i];
     }
 }
 
-// Tokens of a tile: what a block stages in shared memory at a time.
-__host__ __device__ constexpr int tile_tokens(int lpc) { return lpc == 1 ? 8 : lpc <= 16 ? 16 : 32; }
+// Four elements of B or C, as they are stored.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> { using type = float4; };
+template <> struct Raw4<bf16> { using type = uint2; };
+__device__ __forceinline__ void widen(float4 r, float (&v)[4]) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+__device__ __forceinline__ void widen(uint2 r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xffff0000u);
+}
 
-// One block per (channel block, sequence), tokens in order, a tile at a time.  NP state
-// entries a thread, LPC lanes a channel.
+// A thread's two places in a block: a lane of the scan (channel c, entries n0 .. n0+3), and
+// the preparer of the channels gc .. gc+E-1 (of which `count` exist) of token gt of a tile.
+template <int LPC>
+struct Place {
+    static constexpr int CB = kThreads / LPC, TT = tile_tokens(LPC), E = group_channels(LPC);
+    int g, c, n0, li;      // group, channel, entry, channel within the block
+    bool on;
+    int gt, gi, gc, count; // token of the tile, channel within the block, channel
+    __device__ __forceinline__ Place(const Params& p) {
+        const int tid = threadIdx.x, cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
+        g = blockIdx.x / bpg;
+        const int c0 = (blockIdx.x % bpg) * CB;
+        li = tid / LPC;
+        n0 = tid % LPC * 4;
+        on = c0 + li < cpg;
+        c = g * cpg + (on ? c0 + li : 0);
+        gt = tid / (CB / E);
+        gi = tid % (CB / E) * E;
+        count = min(max(cpg - c0 - gi, 0), E);
+        gc = g * cpg + (count > 0 ? c0 + gi : 0);
+    }
+};
+
+template <int LPC>
+struct FwdSmem {
+    static constexpr int N = 4 * LPC, CB = kThreads / LPC, TT = tile_tokens(LPC);
+    float2 du[TT][CB];                 // delta, delta x
+    alignas(16) float bc[2][TT][N];
+    // partial sums of the lanes (of pairs of them where they are 32, to fit 48 KB)
+    static constexpr int YL = LPC < 32 ? LPC : 16;
+    alignas(16) float y[TT][CB][YL];
+};
+
+enum Mode {
+    kOutputs,   // out
+    kStates     // no outputs, but the state before every kSub-th token (the backward's first sweep)
+};
+
+// Tokens [from, to) of sequence n, which starts at token s, from and to the state h of the
+// block's lanes, a tile at a time.
 //
-// A tile passes through three phases.  (1) Each of its (token, channel) pairs has one
-// thread, which forms delta and delta x for all the channel's lanes; B and C become fp32 in
+// A tile passes through three phases.  (1) Each (token, channel) has one thread, which forms
+// delta and delta x for all the channel's lanes, 4 channels at a time; B and C become fp32 in
 // shared memory.  (2) The lanes walk the tile's tokens, with only the state's own chain
-// between them, and sum y over a channel's lanes for LPC tokens at a time.  (3) The
-// pair's thread adds D x, applies the gate and stores.  The next tile's loads are in
-// flight during (2).
-// The exponentials bound it (16 a clock and SM), then the issue slots.
-// CKPT: no outputs, but the state before every kSub-th token (the backward's first sweep).
-template <typename T, int NP, int LPC, bool CKPT>
-__global__ void __launch_bounds__(kThreads)
-fwd_kernel(const __grid_constant__ Params p) {
-    constexpr int N = NP * LPC, TT = tile_tokens(LPC), CB = kThreads / LPC, EL = TT / LPC;
-    constexpr int QUADS = TT * N / 4;                         // of B, and as many of C
-    constexpr int QP = (2 * QUADS + kThreads - 1) / kThreads;
-    __shared__ float2 du_s[TT][CB];                           // delta, delta x
-    __shared__ __align__(16) float bc_s[2][TT][N];
-    __shared__ float y_s[TT][CB + 8];
-    const int n = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    long s, e;
-    if (!p.seq.bounds(n, s, e)) {
-        if (blockIdx.x == 0 && tid == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
-        return;
-    }
-    const int cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
-    const int g = blockIdx.x / bpg, c0 = (blockIdx.x % bpg) * CB;   // first channel within the group
-    // as a lane of the scan: channel and first state entry
-    const bool on = c0 + tid / LPC < cpg;
-    const int c = g * cpg + (on ? c0 + tid / LPC : 0), n0 = (tid % LPC) * NP;
-    const long hrow = ((long)n * p.C + c) * N + n0;
-    Pair A2[NP / 2], h[NP / 2];
+// between them.  (3) The first phase's thread sums y over the lanes, adds D x, applies the
+// gate and stores.  The next tile's loads are in flight during (2).
+template <typename T, int LPC, Mode M, bool VEC>
+__device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Place<LPC>& at, int n, long s, long from,
+                                     long to, const Pair (&A2)[2], Pair (&h)[2]) {
+    constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E;
+    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;   // of B and C
+    const int tid = threadIdx.x;
+    float bias[E], D[E];
 #pragma unroll
-    for (int i = 0; i < NP / 2; ++i) {
-        const float* a = p.A_log + (long)c * N + n0 + 2 * i;
-        A2[i] = pair(-expf(a[0]) * kLog2e, -expf(a[1]) * kLog2e);
-        h[i] = p.h0 ? pair(p.h0[hrow + 2 * i], p.h0[hrow + 2 * i + 1]) : pair(0.f, 0.f);
+    for (int i = 0; i < E; ++i) {
+        bias[i] = p.dt_bias && i < at.count ? p.dt_bias[at.gc + i] : 0.f;
+        D[i] = M == kOutputs && p.D && i < at.count ? p.D[at.gc + i] : 0.f;
     }
-    // as the thread of (token, channel) pairs: channel pc, tokens pt, pt + LPC, ...
-    const int pi = tid % CB, pt = tid / CB;
-    const bool pon = c0 + pi < cpg;
-    const int pc = g * cpg + (pon ? c0 + pi : 0);
-    const float bias = p.dt_bias ? p.dt_bias[pc] : 0.f;
-    const float D = p.D ? p.D[pc] : 0.f;
-
-    T xr[EL], dr[EL], zr[EL];
-    float br[QP][4];
+    Group<T, E> xr, dr, zr;
+    typename Raw4<T>::type br[QP];
+    const bool gated = M == kOutputs && p.z;
     auto fetch = [&](long t0) {
-#pragma unroll
-        for (int k = 0; k < EL; ++k) {
-            const long t = t0 + pt + k * LPC;
-            const bool ok = pon && t < e;
-            const long o = t * p.C + pc;
-            xr[k] = ok ? static_cast<const T*>(p.x)[o] : from_f<T>(0.f);
-            dr[k] = ok ? static_cast<const T*>(p.dt)[o] : from_f<T>(0.f);
-            if (!CKPT && p.z) zr[k] = ok ? static_cast<const T*>(p.z)[o] : from_f<T>(0.f);
-        }
+        const long o = min(t0 + at.gt, to - 1) * p.C + at.gc;
+        xr = load_group<VEC, T, E>(p.x, o, at.count);
+        dr = load_group<VEC, T, E>(p.dt, o, at.count);
+        if (M == kOutputs) zr = load_group<VEC, T, E>(gated ? p.z : p.x, o, at.count);
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * kThreads, which = q / QUADS, r = q % QUADS;
-            const long t = t0 + r / (N / 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) br[k][i] = 0.f;
-            if (which < (CKPT ? 1 : 2) && t < e)
-                load_v<4>(static_cast<const T*>(which ? p.Cm : p.Bm) + (t * p.G + g) * N + r % (N / 4) * 4, br[k]);
+            const int q = tid + k * kThreads, r = q % QUADS;
+            const long tb = min(t0 + r / (N / 4), to - 1);
+            br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
+                static_cast<const T*>(M == kOutputs && q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
         }
     };
-    fetch(s);
-    for (long t0 = s; t0 < e; t0 += TT) {
-        float x[EL], z[EL];
+    fetch(from);
+    for (long t0 = from; t0 < to; t0 += TT) {
+        const bool live = t0 + at.gt < to;
+        const Group<T, E> x = xr, z = zr;
 #pragma unroll
-        for (int k = 0; k < EL; ++k) {
-            const int j = pt + k * LPC;
-            x[k] = to_f(xr[k]);
-            if (!CKPT && p.z) z[k] = to_f(zr[k]);
-            // past the end: delta = 0 leaves the state as it is
-            const float delta = t0 + j < e ? softplus(to_f(dr[k]) + bias) : 0.f;
-            du_s[j][pi] = make_float2(delta, delta * x[k]);
+        for (int i = 0; i < E; ++i) {
+            // past the end: delta = 0 and delta x = 0 leave the state as it is
+            const float delta = softplus(to_f(dr.v[i]) + bias[i]);
+            sm.du[at.gt][at.gi + i] = live ? make_float2(delta, delta * to_f(x.v[i])) : make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
             const int q = tid + k * kThreads;
-            if (q < 2 * QUADS) store_v<4>(&bc_s[0][0][0] + q * 4, br[k]);
+            float v[4];
+            widen(br[k], v);
+            const bool in = t0 + q % QUADS / (N / 4) < to;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
+            if (q < 2 * QUADS) store_v<4>(&sm.bc[0][0][0] + q * 4, v);
         }
         __syncthreads();
-        if (t0 + TT < e) fetch(t0 + TT);
+        if (t0 + TT < to) fetch(t0 + TT);
+        // kBatch tokens at a time: their operands are read, and their decays and inputs formed,
+        // before the previous batch's y is stored (a store would hold back later loads)
+        float2 du[kBatch];
+        Pair b[kBatch][2], c[kBatch][2];
+        auto operands = [&](int j0) {
 #pragma unroll
-        for (int j0 = 0; j0 < TT; j0 += LPC) {
-            float y[LPC];
+            for (int j = 0; j < kBatch; ++j) {
+                du[j] = sm.du[j0 + j][at.li];
+                load_pairs<4>(&sm.bc[0][j0 + j][at.n0], b[j]);
+            }
+        };
+        operands(0);
 #pragma unroll
-            for (int jj = 0; jj < LPC; ++jj) {
-                const int j = j0 + jj;
-                if (CKPT && j % kSub == 0 && on && t0 + j < e) {
-                    store_pairs<NP>(p.ckpt + (ckpt_slot(s, n, (t0 - s + j) / kSub) * p.C + c) * N + n0, h);
+        for (int j0 = 0; j0 < TT; j0 += kBatch) {
+            Pair a[kBatch][2];
+            float y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    a[j][i] = exp2_pair(mul2(dl, A2[i]));
+                    b[j][i] = mul2(u, b[j][i]);
                 }
-                const float2 du = du_s[j][tid / LPC];
-                const Pair dl = pair(du.x, du.x), u = pair(du.y, du.y);
-                Pair b[NP / 2], cc[NP / 2], acc;
-                load_pairs<NP>(&bc_s[0][j][n0], b);
-                if (!CKPT) load_pairs<NP>(&bc_s[1][j][n0], cc);
+                if (M == kOutputs) load_pairs<4>(&sm.bc[1][j0 + j][at.n0], c[j]);
+            }
 #pragma unroll
-                for (int i = 0; i < NP / 2; ++i) {
-                    h[i] = fma2(exp2_pair(mul2(dl, A2[i])), h[i], mul2(u, b[i]));
-                    if (!CKPT) acc = i == 0 ? mul2(h[i], cc[i]) : fma2(h[i], cc[i], acc);
-                }
-                if (!CKPT) {
+            for (int j = 0; j < kBatch; ++j) {
+                if (M == kStates && (j0 + j) % kSub == 0 && at.on && t0 + j0 + j < to)
+                    store_pairs<4>(p.ckpt + (ckpt_slot(s, n, (t0 - s + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
+                h[0] = fma2(a[j][0], h[0], b[j][0]);
+                h[1] = fma2(a[j][1], h[1], b[j][1]);
+                if (M == kOutputs) {
                     float lo, hi;
-                    unpair(acc, lo, hi);
-                    y[jj] = lo + hi;
+                    unpair(fma2(h[1], c[j][1], mul2(h[0], c[j][0])), lo, hi);
+                    y[j] = lo + hi;
+                    if (LPC > FwdSmem<LPC>::YL) y[j] += __shfl_xor_sync(0xffffffffu, y[j], 1);
                 }
             }
-            if (!CKPT) {
-                transpose_sum<LPC, 1>(y, lane);
-                y_s[j0 + tid % LPC][tid / LPC] = y[0];
-            }
+            if (j0 + kBatch < TT) operands(j0 + kBatch);
+            if (M == kOutputs)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) sm.y[j0 + j][at.li][tid % LPC / (LPC / FwdSmem<LPC>::YL)] = y[j];
         }
         __syncthreads();
-        if (!CKPT) {
+        if (M == kOutputs && live && at.count > 0) {
+            float y[E];
 #pragma unroll
-            for (int k = 0; k < EL; ++k) {
-                const int j = pt + k * LPC;
-                if (!pon || t0 + j >= e) continue;
-                float y = fmaf(D, x[k], y_s[j][pi]);
-                if (p.z) y *= silu(z[k]);
-                static_cast<T*>(p.out)[(t0 + j) * p.C + pc] = from_f<T>(y);
+            for (int i = 0; i < E; ++i) {
+                const float* l = sm.y[at.gt][at.gi + i];
+                y[i] = l[0] + l[1];
+#pragma unroll
+                for (int k = 2; k < FwdSmem<LPC>::YL; k += 2) y[i] += l[k] + l[k + 1];
+                y[i] = fmaf(D[i], to_f(x.v[i]), y[i]);
+                if (gated) y[i] *= silu(to_f(z.v[i]));
             }
+            store_group<VEC, T, E>(p.out, (t0 + at.gt) * p.C + at.gc, y, at.count);
         }
     }
-    if (!CKPT && p.h_final && on) store_pairs<NP>(p.h_final + hrow, h);
+}
+
+template <int LPC>
+__device__ __forceinline__ void load_decays(const Params& p, const Place<LPC>& at, Pair (&A2)[2]) {
+    float a[4];
+    load_v<4>(p.A_log + (long)at.c * (4 * LPC) + at.n0, a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) A2[i] = pair(-expf(a[2 * i]) * kLog2e, -expf(a[2 * i + 1]) * kLog2e);
+}
+
+// One block per (channel block, sequence).
+template <typename T, int LPC, Mode M, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+fwd_kernel(const __grid_constant__ Params p) {
+    __shared__ FwdSmem<LPC> sm;
+    const Place<LPC> at(p);
+    const int n = blockIdx.y;
+    long s, e;
+    if (!p.seq.bounds(n, s, e)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
+        return;
+    }
+    const long hrow = ((long)n * p.C + at.c) * (4 * LPC) + at.n0;
+    Pair A2[2], h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    load_decays<LPC>(p, at, A2);
+    if (p.h0) load_pairs<4>(p.h0 + hrow, h);
+    walk<T, LPC, M, VEC>(p, sm, at, n, s, s, e, A2, h);
+    if (M == kOutputs && p.h_final && at.on) store_pairs<4>(p.h_final + hrow, h);
 }
 
 // Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state

@@ -440,7 +440,7 @@ int comba_short_conv_step(const void* x, const float* weight, const float* bias,
  * x, dt, z, out: token tensors of C channels (z NULL: out = y).  Bm, Cm: [tokens, G, N].
  * A_log [C, N], D [C] or NULL (zero), dt_bias [C] or NULL (zero), h0 and h_final
  * [nseq, C, N]: fp32 (h0 NULL: zero; h_final NULL: not written; h_final may be h0 itself,
- * but overlap it in no other way).  G must divide C; N in {4, 8, 16, 32, 64, 128}.  A_log,
+ * but overlap it in no other way).  G must divide C; N in {8, 16, 32, 64, 128}.  A_log,
  * Bm, Cm, h0 and h_final 16-byte aligned.  nseq <= 65535 (COMBA_EUNSUPPORTED above).
  */
 int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,

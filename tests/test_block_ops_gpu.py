@@ -169,7 +169,7 @@ SCAN_CASES = [  # lengths, C, G, N, dtype, options: D skip, dt bias, z gate, h s
     ([9, 9, 9], 130, 2, 16, BF, "bh"),
     ([8, 8], 96, 3, 8, F32, "Dz"),
     ([1, 1], 33, 1, 16, F32, "Dbzh"),
-    ([7], 6, 2, 4, BF, ""),
+    ([7], 6, 2, 8, BF, ""),
     ([65, 65], 40, 1, 32, F32, "Dbzh"),
     ([40], 20, 2, 64, BF, "Dbzh"),
     ([23], 10, 1, 128, F32, "bzh"),
