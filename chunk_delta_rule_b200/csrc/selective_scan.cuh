@@ -147,6 +147,8 @@ __device__ __forceinline__ void store_group(void* base, long o, const float (&f)
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Four elements of B or C, as they are stored.
 template <typename T> struct Raw4;
 template <> struct Raw4<float> { using type = float4; };
@@ -190,6 +192,18 @@ struct FwdSmem {
     alignas(16) float y[TT][CB][YL];
 };
 
+// Where channel `ch` of token t lies in a row of du and of y: permuted within four
+// neighbours, so that the preparers (4 channels a thread) and the lanes (one channel each)
+// both touch different banks (for 8 to 32 lanes a channel, y's reads keep conflicts).
+template <int LPC>
+__device__ __forceinline__ int du_slot(int t, int ch) {
+    return group_channels(LPC) == 4 ? ch ^ (((ch >> 4) & 1) | ((t & 1) << 1)) : ch;
+}
+template <int LPC>
+__device__ __forceinline__ int y_slot(int ch) {
+    return group_channels(LPC) == 4 ? ch ^ ((ch >> (LPC == 2 ? 4 : LPC == 4 ? 3 : 2)) & 3) : ch;
+}
+
 enum Mode {
     kOutputs,   // out
     kStates     // no outputs, but the state before every kSub-th token (the backward's first sweep)
@@ -208,7 +222,8 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
                                      long to, const Pair (&A2)[2], Pair (&h)[2]) {
     constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E;
     constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;   // of B and C
-    const int tid = threadIdx.x;
+    if (from >= to) return;   // fetch() needs a last token to clamp to
+    const int tid = threadIdx.x, ys = y_slot<LPC>(at.li);
     float bias[E], D[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -223,6 +238,10 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         xr = load_group<VEC, T, E>(p.x, o, at.count);
         dr = load_group<VEC, T, E>(p.dt, o, at.count);
         if (M == kOutputs) zr = load_group<VEC, T, E>(gated ? p.z : p.x, o, at.count);
+        const long ahead = min(t0 + 2 * TT + at.gt, to - 1) * p.C + at.gc;
+        prefetch_l2(static_cast<const T*>(p.x) + ahead);
+        prefetch_l2(static_cast<const T*>(p.dt) + ahead);
+        if (gated) prefetch_l2(static_cast<const T*>(p.z) + ahead);
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
             const int q = tid + k * kThreads, r = q % QUADS;
@@ -239,7 +258,7 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         for (int i = 0; i < E; ++i) {
             // past the end: delta = 0 and delta x = 0 leave the state as it is
             const float delta = softplus(to_f(dr.v[i]) + bias[i]);
-            sm.du[at.gt][at.gi + i] = live ? make_float2(delta, delta * to_f(x.v[i])) : make_float2(0.f, 0.f);
+            sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)] = live ? make_float2(delta, delta * to_f(x.v[i])) : make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
@@ -260,7 +279,7 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         auto operands = [&](int j0) {
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                du[j] = sm.du[j0 + j][at.li];
+                du[j] = sm.du[j0 + j][du_slot<LPC>(j0 + j, at.li)];
                 load_pairs<4>(&sm.bc[0][j0 + j][at.n0], b[j]);
             }
         };
@@ -295,14 +314,14 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
             if (j0 + kBatch < TT) operands(j0 + kBatch);
             if (M == kOutputs)
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) sm.y[j0 + j][at.li][tid % LPC / (LPC / FwdSmem<LPC>::YL)] = y[j];
+                for (int j = 0; j < kBatch; ++j) sm.y[j0 + j][ys][tid % LPC / (LPC / FwdSmem<LPC>::YL)] = y[j];
         }
         __syncthreads();
         if (M == kOutputs && live && at.count > 0) {
             float y[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float* l = sm.y[at.gt][at.gi + i];
+                const float* l = sm.y[at.gt][y_slot<LPC>(at.gi + i)];
                 y[i] = l[0] + l[1];
 #pragma unroll
                 for (int k = 2; k < FwdSmem<LPC>::YL; k += 2) y[i] += l[k] + l[k + 1];
