@@ -38,7 +38,7 @@ EXPORTS = ("comba_chunk_fwd", "comba_chunk_fwd_f32", "comba_chunk_fwd_varlen",
            "comba_chunk_fwd_transition", "comba_chunk_fwd_stall_test", "comba_chunk_bwd_stall_test",
            "comba_recurrent_step", "comba_recurrent_step_grouped",
            "comba_short_conv_fwd", "comba_short_conv_bwd", "comba_short_conv_bwd_workspace_size",
-           "comba_short_conv_step", "comba_selective_scan_fwd", "comba_selective_scan_bwd",
+           "comba_short_conv_step", "comba_selective_scan_fwd", "comba_selective_scan_fwd_workspace_size", "comba_selective_scan_bwd",
            "comba_selective_scan_bwd_workspace_size", "comba_selective_scan_step",
            "comba_gated_norm_fwd", "comba_gated_norm_bwd", "comba_gated_norm_bwd_workspace_size",
            "comba_residual_norm_fwd", "comba_residual_norm_bwd", "comba_residual_norm_bwd_workspace_size",
@@ -94,7 +94,8 @@ def library():
                     ("comba_short_conv_bwd", [vp] * 11 + [i] * 6 + [vp, sz, vp], i),
                     ("comba_short_conv_bwd_workspace_size", [i] * 5, sz),
                     ("comba_short_conv_step", [vp] * 5 + [i] * 5 + [vp], i),
-                    ("comba_selective_scan_fwd", [vp] * 12 + [i] * 6 + [vp], i),
+                    ("comba_selective_scan_fwd", [vp] * 12 + [i] * 6 + [vp, sz, vp], i),
+                    ("comba_selective_scan_fwd_workspace_size", [i] * 6, sz),
                     ("comba_selective_scan_bwd", [vp] * 21 + [i] * 6 + [vp, sz, vp], i),
                     ("comba_selective_scan_bwd_workspace_size", [i] * 6, sz),
                     ("comba_selective_scan_step", [vp] * 10 + [i] * 5 + [vp], i),

@@ -188,13 +188,15 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: t
                    z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
                    cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                    h_final: Optional[torch.Tensor] = None, return_state: bool = True,
-                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """comba_selective_scan_fwd: h_t = exp(delta A) h_{t-1} + delta x_t B_t, out_t =
     (sum_n h_t C_t + D x_t) silu(z_t), with delta = softplus(dt + dt_bias) and A =
     -exp(A_log).  x, dt, z [B,T,C] or packed [total_T,C], bf16 or fp32; Bm, Cm [...,G,N]
     of the same type (G dividing C; N 8 .. 128, a power of two); A_log [C,N], D and
     dt_bias [C] (or None), h0 [nseq,C,N] (or None) fp32.  Returns (out like x, h_final
-    [nseq,C,N] fp32 or None).  ``h_final`` may be passed as ``h0`` itself."""
+    [nseq,C,N] fp32 or None).  ``h_final`` may be passed as ``h0`` itself.  ``workspace``: a
+    uint8 device tensor of at least comba_selective_scan_fwd_workspace_size bytes (few long
+    sequences run in pieces), for this call alone."""
     lead, nseq, T, C = _tokens(x, cu_seqlens)
     G, N = _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
     et, dev = x.dtype, x.device
@@ -207,8 +209,10 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: t
     if h_final is None and return_state:
         h_final = call.new((nseq, C, N), torch.float32)
     _tensor(h_final, "h_final", torch.float32, (nseq, C, N), dev, True)
+    need = _cdr.library().comba_selective_scan_fwd_workspace_size(nseq, T, C, G, N, int(cu_seqlens is not None))
+    ws = call.workspace(need, workspace) if need or workspace is not None else None
     call("comba_selective_scan_fwd", x, dt, A_log, Bm, Cm, D, dt_bias, z, h0, out, h_final, cu_seqlens, nseq, T, C, G, N,
-         _DTYPE[et])
+         _DTYPE[et], ws, 0 if ws is None else ws.numel())
     return out, h_final
 
 

@@ -3,6 +3,8 @@
 //
 // As in comba.cu, every argument is checked before anything is enqueued, work goes on the
 // caller's stream, and no device memory is owned or allocated.
+#include <algorithm>
+
 #include "block_norm.cuh"
 #include "selective_scan.cuh"
 #include "short_conv.cuh"
@@ -223,9 +225,57 @@ ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
     return w;
 }
 
+// Pieces of the split form, 1 for the direct one.  Costs in clocks of an SM for 16 tokens of
+// a channel block, measured on B8 and B1 T4096..64K C2048 N16: 2950 where a block has its SM to
+// itself (latency), 1290 where 4 share it, and 700 for the split form's first sweep.  A packed
+// batch's longest sequence is taken to be 4 times the mean.
+int scan_pieces(const Seqs& q, int C, int G, int N) {
+    const double sm_blocks = (double)G * group_blocks(C, G, N) / kSMs;
+    const double tiles = q.tokens() / 16.0, mean = tiles / q.N;
+    const double longest = q.cu ? (4 * mean < tiles ? 4 * mean : tiles) : mean;
+    const double direct = std::max(longest * 2950, tiles * sm_blocks * 1290), split = tiles * sm_blocks * (1290 + 700);
+    const long most = std::min<long>(128, q.tokens() / 128);
+    const long fit = (long)(4 / sm_blocks);      // one wave of 4 blocks an SM
+    const long pieces = std::min(most, fit);
+    return pieces >= 2 && split * std::max(1.0, fit / (double)pieces) < direct ? (int)pieces : 1;
+}
+
+// The split form's cut and workspace; `pieces` may come out smaller for the rounding.
+struct SplitWs {
+    long piece = 0;
+    int pieces = 1;
+    size_t ends = 0, dsum = 0, h0 = 0, total = 0;
+};
+SplitWs split_ws(const Seqs& q, int C, int G, int N) {
+    SplitWs w;
+    const int want = q.tokens() > 0 ? scan_pieces(q, C, G, N) : 1;
+    if (want < 2) return w;
+    w.piece = ceil_div(ceil_div(q.tokens(), want), 32) * 32;
+    w.pieces = (int)ceil_div(q.tokens(), w.piece);
+    size_t o = 0;
+    auto take = [&](size_t n) { const size_t at = o; o += (n + 255) & ~(size_t)255; return at; };
+    w.ends = take((size_t)w.pieces * C * N * 4);
+    w.dsum = take((size_t)w.pieces * C * 4);
+    w.h0 = take((size_t)q.N * C * N * 4);
+    w.total = o;
+    return w;
+}
+
 template <typename T, int LPC>
 int scan_fwd(const scan::Params& p, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
+    const unsigned bx = (unsigned)(p.G * group_blocks(p.C, p.G, p.N));
+    if (p.pieces > 1) {
+        const dim3 grid(bx, (unsigned)p.pieces);
+        if (p.vec) {
+            scan::ends_kernel<T, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
+            scan::split_kernel<T, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
+        } else {
+            scan::ends_kernel<T, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
+            scan::split_kernel<T, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
+        }
+        return launched();
+    }
+    const dim3 grid(bx, (unsigned)p.seq.N);
     if (p.vec) scan::fwd_kernel<T, LPC, scan::kOutputs, true><<<grid, scan::kThreads, 0, s>>>(p);
     else scan::fwd_kernel<T, LPC, scan::kOutputs, false><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
@@ -278,10 +328,16 @@ int scan_sizes(int nseq, int T, int C, int G, int N, int dtype, size_t tokens) {
 
 }  // namespace
 
+extern "C" size_t comba_selective_scan_fwd_workspace_size(int nseq, int T, int C, int G, int N, int packed) {
+    if (nseq <= 0 || T < 0 || C <= 0 || G < 1 || C % G || !states_ok(N)) return 0;
+    const int any = 0;
+    return split_ws(Seqs{packed ? &any : nullptr, nseq, T}, C, G, N).total;
+}
+
 extern "C" int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
                                         const float* D, const float* dt_bias, const void* z, const float* h0, void* out,
                                         float* h_final, const int* cu_seqlens, int nseq, int T, int C, int G, int N,
-                                        int dtype, comba_stream_t stream) {
+                                        int dtype, void* workspace, size_t workspace_bytes, comba_stream_t stream) {
     const size_t tokens = nseq > 0 && T > 0 ? token_count(cu_seqlens, nseq, T) : 0;
     if (int st = scan_sizes(nseq, T, C, G, N, dtype, tokens)) return st;
     if (nseq == 0 || C == 0) return COMBA_OK;
@@ -290,17 +346,32 @@ extern "C" int comba_selective_scan_fwd(const void* x, const void* dt, const flo
                        {Cm, nb, 16, false}, {D, (size_t)C * 4, 4, true}, {dt_bias, (size_t)C * 4, 4, true},
                        {z, nx, e, true}, {h0 == h_final ? nullptr : h0, ns, 16, true},
                        {cu_seqlens, ((size_t)nseq + 1) * 4, 4, true}};
-    const Arg outs[] = {{out, nx, e, false}, {h_final, ns, 16, true}};
+    const Seqs seq{cu_seqlens, nseq, T};
+    const SplitWs ws = split_ws(seq, C, G, N);
+    if (workspace_bytes < ws.total) return COMBA_EINVAL;
+    const Arg outs[] = {{out, nx, e, false}, {h_final, ns, 16, true}, {workspace, ws.total, 16, false}};
     if (!args_ok(ins, outs)) return COMBA_EINVAL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     scan::Params p{};
     p.x = x; p.dt = dt; p.A_log = A_log; p.Bm = Bm; p.Cm = Cm; p.D = D; p.dt_bias = dt_bias; p.z = z; p.h0 = h0;
     p.out = out; p.h_final = h_final;
-    p.seq = Seqs{cu_seqlens, nseq, T};
+    p.seq = seq;
     p.C = C; p.G = G; p.N = N;
     p.vec = scan_vector(C, G, N, dtype, {x, dt, z, out});
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
-    return COMBA_SCAN_DISPATCH(scan_fwd, dtype, N, p, reinterpret_cast<cudaStream_t>(stream));
+    p.piece = ws.piece;
+    p.pieces = ws.pieces;
+    if (ws.pieces > 1) {
+        char* w = static_cast<char*>(workspace);
+        p.ends = reinterpret_cast<float*>(w + ws.ends);
+        p.dsum = reinterpret_cast<float*>(w + ws.dsum);
+        if (h0 && h0 == h_final) {   // one block's final state must not replace another's start
+            if (cudaMemcpyAsync(w + ws.h0, h0, ns, cudaMemcpyDeviceToDevice, s) != cudaSuccess) return COMBA_ECUDA;
+            p.h0 = reinterpret_cast<const float*>(w + ws.h0);
+        }
+    }
+    return COMBA_SCAN_DISPATCH(scan_fwd, dtype, N, p, s);
 }
 
 extern "C" size_t comba_selective_scan_bwd_workspace_size(int nseq, int T, int C, int G, int N, int packed) {

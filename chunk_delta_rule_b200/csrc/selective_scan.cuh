@@ -26,6 +26,10 @@ struct Params {
     const float *A_log, *D, *dt_bias, *h0, *dh_final;
     void *out, *dx, *ddt, *dz;
     float *h_final, *dh0;
+    long piece;                  // split form: tokens of a piece of the joint token axis
+    int pieces;
+    float* ends;                 // [pieces, C, N]: state after a piece (see ends_kernel)
+    float* dsum;                 // [pieces, C]: sum of delta over it
     float* ckpt;                 // [slots, C, N]: the state before every kSub-th token of a sequence
     float* part_bc;              // [channel blocks, tokens, 2, N]
     double* part_a;              // [sequences, C, N]
@@ -206,7 +210,8 @@ __device__ __forceinline__ int y_slot(int ch) {
 
 enum Mode {
     kOutputs,   // out
-    kStates     // no outputs, but the state before every kSub-th token (the backward's first sweep)
+    kStates,    // no outputs, but the state before every kSub-th token (the backward's first sweep)
+    kEnds       // no outputs, only the state after the last token (the split form's first sweep)
 };
 
 // Tokens [from, to) of sequence n, which starts at token s, from and to the state h of the
@@ -219,7 +224,7 @@ enum Mode {
 // gate and stores.  The next tile's loads are in flight during (2).
 template <typename T, int LPC, Mode M, bool VEC>
 __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Place<LPC>& at, int n, long s, long from,
-                                     long to, const Pair (&A2)[2], Pair (&h)[2]) {
+                                     long to, const Pair (&A2)[2], Pair (&h)[2], float& dsum) {
     constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E;
     constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;   // of B and C
     if (from >= to) return;   // fetch() needs a last token to clamp to
@@ -287,13 +292,14 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
 #pragma unroll
         for (int j0 = 0; j0 < TT; j0 += kBatch) {
             Pair a[kBatch][2];
-            float y[kBatch];
+            float y[kBatch], dl[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y);
+                dl[j] = du[j].x;
+                const Pair d2 = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    a[j][i] = exp2_pair(mul2(dl, A2[i]));
+                    a[j][i] = exp2_pair(mul2(d2, A2[i]));
                     b[j][i] = mul2(u, b[j][i]);
                 }
                 if (M == kOutputs) load_pairs<4>(&sm.bc[1][j0 + j][at.n0], c[j]);
@@ -304,6 +310,7 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
                     store_pairs<4>(p.ckpt + (ckpt_slot(s, n, (t0 - s + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
                 h[0] = fma2(a[j][0], h[0], b[j][0]);
                 h[1] = fma2(a[j][1], h[1], b[j][1]);
+                if (M == kEnds) dsum += dl[j];
                 if (M == kOutputs) {
                     float lo, hi;
                     unpair(fma2(h[1], c[j][1], mul2(h[0], c[j][0])), lo, hi);
@@ -355,10 +362,89 @@ fwd_kernel(const __grid_constant__ Params p) {
     }
     const long hrow = ((long)n * p.C + at.c) * (4 * LPC) + at.n0;
     Pair A2[2], h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    float dsum;
     load_decays<LPC>(p, at, A2);
     if (p.h0) load_pairs<4>(p.h0 + hrow, h);
-    walk<T, LPC, M, VEC>(p, sm, at, n, s, s, e, A2, h);
+    walk<T, LPC, M, VEC>(p, sm, at, n, s, s, e, A2, h, dsum);
     if (M == kOutputs && p.h_final && at.on) store_pairs<4>(p.h_final + hrow, h);
+}
+
+// The split form, for too few (channel block, sequence) pairs to fill the GPU: the joint
+// token axis is cut into pieces, which run as blocks of their own.  Over a piece, a channel's
+// entry goes from h to exp(A sum delta) h + r.
+//
+// First sweep: for a piece that ends inside a sequence, r from that sequence's tokens in it
+// (from h0 where the sequence starts there, so that r is the state itself) and sum delta.
+template <typename T, int LPC, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+ends_kernel(const __grid_constant__ Params p) {
+    __shared__ FwdSmem<LPC> sm;
+    const Place<LPC> at(p);
+    const long t0 = blockIdx.y * p.piece, t1 = min(t0 + p.piece, p.seq.tokens());
+    const int n = p.seq.find(t1 - 1);
+    long s, e;
+    if (!p.seq.bounds(n, s, e) || s >= t1 || e <= t1) return;
+    Pair A2[2], h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    float dsum = 0.f;
+    load_decays<LPC>(p, at, A2);
+    if (s >= t0 && p.h0) load_pairs<4>(p.h0 + ((long)n * p.C + at.c) * (4 * LPC) + at.n0, h);
+    walk<T, LPC, kEnds, VEC>(p, sm, at, n, s, max(s, t0), t1, A2, h, dsum);
+    if (!at.on) return;
+    const long row = (long)blockIdx.y * p.C + at.c;
+    store_pairs<4>(p.ends + row * (4 * LPC) + at.n0, h);
+    if (at.n0 == 0) p.dsum[row] = dsum;
+}
+
+// Second sweep: every piece again, each sequence in it from its start state, which the
+// block composes from the pieces before it.
+template <typename T, int LPC, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+split_kernel(const __grid_constant__ Params p) {
+    constexpr int N = 4 * LPC;
+    __shared__ FwdSmem<LPC> sm;
+    const Place<LPC> at(p);
+    const int j = blockIdx.y;
+    for (int n = j; n < p.seq.N; n += p.pieces) {   // sequences without tokens, and bad bounds
+        long s, e;
+        const bool ok = p.seq.bounds(n, s, e);
+        if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
+        if (!ok || s < e || !p.h_final || !at.on) continue;
+        Pair h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const long hrow = ((long)n * p.C + at.c) * N + at.n0;
+        if (p.h0) load_pairs<4>(p.h0 + hrow, h);
+        store_pairs<4>(p.h_final + hrow, h);
+    }
+    Pair A2[2];
+    float dsum;
+    load_decays<LPC>(p, at, A2);
+    const long t0 = j * p.piece, t1 = min(t0 + p.piece, p.seq.tokens());
+    long t = t0;
+    for (int n = p.seq.find(t0); n < p.seq.N && t < t1; ++n) {
+        long s, e;
+        if (!p.seq.bounds(n, s, e) || e <= t) continue;
+        if (s >= t1) break;
+        t = max(t, s);
+        const long hrow = ((long)n * p.C + at.c) * N + at.n0, stop = min(e, t1);
+        Pair h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        if (t == s) {
+            if (p.h0) load_pairs<4>(p.h0 + hrow, h);
+        } else {
+            const int j0 = (int)(s / p.piece);
+            load_pairs<4>(p.ends + ((long)j0 * p.C + at.c) * N + at.n0, h);
+#pragma unroll 4
+            for (int i = j0 + 1; i < j; ++i) {
+                const long row = (long)i * p.C + at.c;
+                const float ds = p.dsum[row];
+                Pair r[2];
+                load_pairs<4>(p.ends + row * N + at.n0, r);
+                h[0] = fma2(exp2_pair(mul2(pair(ds, ds), A2[0])), h[0], r[0]);
+                h[1] = fma2(exp2_pair(mul2(pair(ds, ds), A2[1])), h[1], r[1]);
+            }
+        }
+        walk<T, LPC, kOutputs, VEC>(p, sm, at, n, s, t, stop, A2, h, dsum);
+        if (stop == e && p.h_final && at.on) store_pairs<4>(p.h_final + hrow, h);
+        t = stop;
+    }
 }
 
 // Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state

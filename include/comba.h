@@ -442,11 +442,15 @@ int comba_short_conv_step(const void* x, const float* weight, const float* bias,
  * [nseq, C, N]: fp32 (h0 NULL: zero; h_final NULL: not written; h_final may be h0 itself,
  * but overlap it in no other way).  G must divide C; N in {8, 16, 32, 64, 128}.  A_log,
  * Bm, Cm, h0 and h_final 16-byte aligned.  nseq <= 65535 (COMBA_EUNSUPPORTED above).
+ * The workspace may be of size 0 (and NULL): it is for the split form, which cuts few long
+ * sequences into pieces and joins them by their state transitions; equal up to rounding.
+ * `packed` in the workspace size says whether cu_seqlens is given.
  */
+size_t comba_selective_scan_fwd_workspace_size(int nseq, int T, int C, int G, int N, int packed);
 int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
                              const float* D, const float* dt_bias, const void* z, const float* h0, void* out,
                              float* h_final, const int* cu_seqlens, int nseq, int T, int C, int G, int N,
-                             int dtype, comba_stream_t stream);
+                             int dtype, void* workspace, size_t workspace_bytes, comba_stream_t stream);
 
 /*
  * Gradients of <dout, out> + <dh_final, h_final> of comba_selective_scan_fwd with respect

@@ -205,6 +205,32 @@ def test_scan(lengths, C, G, N, dtype, opts, packed):
     assert cdr.get_last_error() == 0
 
 
+@pytest.mark.parametrize("lengths,C,G,N,dtype", [([1000], 33, 1, 16, F32), ([700, 700], 64, 2, 8, BF), ([1537], 24, 1, 64, BF),
+                                                 ([3, 0, 900, 1, 0, 130, 640, 0], 40, 1, 16, F32),
+                                                 ([256, 256, 0, 512, 31, 1], 16, 1, 32, BF), ([0, 0, 1500, 0], 10, 1, 128, F32)])
+def test_scan_in_pieces(lengths, C, G, N, dtype):
+    # few channels and many tokens: the split form.  Some sequences end, start or are empty
+    # where a piece does; the state is carried in place.
+    b, n = bounds_of(lengths), len(lengths)
+    packed = len(set(lengths)) > 1
+    assert cdr.library().comba_selective_scan_fwd_workspace_size(n, b[-1] if packed else lengths[0], C, G, N, int(packed)) > 0
+    h = scan_inputs(b[-1], n, C, G, N, dtype, 5 + n, "Dbzh")
+    h["dt_bias"] -= 2          # decays slow enough for the pieces to matter
+    lead = (b[-1],) if packed else (n, lengths[0])
+    cu = torch.tensor(b, dtype=torch.int32, device="cuda") if packed else None
+    a, kw, v = scan_args(dev(h), lead)
+    ro, rh, _ = scan_reference(h, b, backward=False)
+    out, hf = cdr.selective_scan(*a, **kw, cu_seqlens=cu)
+    # twice the roundings of 300 tokens and more of them: sqrt(1600 / 300) times SCAN
+    check("out", out.view(-1, C), ro, 3 * SCAN + HALF[dtype])
+    check("h_final", hf, rh, 3 * SCAN)
+    state = kw["h0"].clone()
+    out2, _ = cdr.selective_scan(*a, **dict(kw, h0=state), h_final=state, cu_seqlens=cu)
+    assert torch.equal(out2, out) and torch.equal(state, hf)
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == 0
+
+
 def test_scan_gradients_against_differences():
     # The kernel's gradient along a random direction of every input against a central
     # difference of the float64 definition: its error is h^2 times a third derivative of

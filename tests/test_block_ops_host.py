@@ -28,7 +28,7 @@ CALLS = {
                              dict(N=2, T=64, C=32, W=4, silu=1, dtype=0, ws=BASE + 40 * GB, nws=1 << 24)),
     "comba_short_conv_step": (["x", "weight", "bias", "state", "out"], dict(B=2, C=32, W=4, silu=1, dtype=0)),
     "comba_selective_scan_fwd": (["x", "dt", "A_log", "Bm", "Cm", "D", "bias", "z", "h0", "out", "hf", "cu"],
-                                 dict(n=2, T=64, C=32, G=2, N=16, dtype=0)),
+                                 dict(n=2, T=4096, C=32, G=2, N=16, dtype=0, ws=BASE + 40 * GB, nws=1 << 24)),
     "comba_selective_scan_bwd": (["x", "dt", "A_log", "Bm", "Cm", "D", "bias", "z", "h0", "dout", "dhf", "dx", "ddt", "dA",
                                   "dBm", "dCm", "dD", "dbias", "dz", "dh0", "cu"],
                                  dict(n=2, T=64, C=32, G=2, N=16, dtype=0, ws=BASE + 40 * GB, nws=1 << 28)),
@@ -63,7 +63,7 @@ REFUSED = []
 for _n, _required in [("comba_short_conv_fwd", ["x", "weight", "out"]),
                       ("comba_short_conv_bwd", ["x", "weight", "dout", "dx", "dweight", "ws"]),
                       ("comba_short_conv_step", ["x", "weight", "state", "out"]),
-                      ("comba_selective_scan_fwd", ["x", "dt", "A_log", "Bm", "Cm", "out"]),
+                      ("comba_selective_scan_fwd", ["x", "dt", "A_log", "Bm", "Cm", "out", "ws"]),
                       ("comba_selective_scan_bwd", ["x", "dt", "A_log", "Bm", "Cm", "dout", "dx", "ddt", "dA", "dBm", "dCm", "ws"]),
                       ("comba_selective_scan_step", ["x", "dt", "A_log", "Bm", "Cm", "h", "out"]),
                       ("comba_gated_norm_fwd", ["x", "gate", "weight", "out"]),
@@ -129,6 +129,11 @@ def test_workspace_sizes(lib):
     # N uniform sequences of T tokens, or T packed tokens
     assert lib.comba_short_conv_bwd_workspace_size(2, 64, 32, 4, 0) == lib.comba_short_conv_bwd_workspace_size(9, 128, 32, 4, 1)
     assert lib.comba_selective_scan_bwd_workspace_size(2, 64, 32, 5, 16, 0) == 0
+    # few long sequences are cut into pieces; many, or short ones, are not
+    assert lib.comba_selective_scan_fwd_workspace_size(1, 65536, 256, 1, 16, 0) > 0
+    assert lib.comba_selective_scan_fwd_workspace_size(1, 65536, 256, 1, 16, 1) > 0
+    assert lib.comba_selective_scan_fwd_workspace_size(64, 1024, 2048, 1, 16, 0) == 0
+    assert lib.comba_selective_scan_fwd_workspace_size(1, 100, 256, 1, 16, 0) == 0
     assert (lib.comba_selective_scan_bwd_workspace_size(2, 4096, 32, 2, 16, 0)
             > lib.comba_selective_scan_bwd_workspace_size(2, 64, 32, 2, 16, 0) > 0)
     assert lib.comba_residual_norm_bwd_workspace_size(100, 64) == 3 * lib.comba_gated_norm_bwd_workspace_size(100, 64) > 0
