@@ -286,7 +286,16 @@ int scan_bwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
     if (p.vec) scan::fwd_kernel<T, LPC, scan::kStates, true><<<grid, scan::kThreads, 0, s>>>(p);
     else scan::fwd_kernel<T, LPC, scan::kStates, false><<<grid, scan::kThreads, 0, s>>>(p);
-    scan::bwd_kernel<T, LPC><<<grid, scan::kThreads, 0, s>>>(p);
+    constexpr int smem = (int)sizeof(scan::BwdSmem<LPC>);
+    if (p.vec) {
+        if (cudaFuncSetAttribute(scan::bwd_kernel<T, LPC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return COMBA_ECUDA;
+        scan::bwd_kernel<T, LPC, true><<<grid, scan::kThreads, smem, s>>>(p);
+    } else {
+        if (cudaFuncSetAttribute(scan::bwd_kernel<T, LPC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return COMBA_ECUDA;
+        scan::bwd_kernel<T, LPC, false><<<grid, scan::kThreads, smem, s>>>(p);
+    }
     return launched();
 }
 

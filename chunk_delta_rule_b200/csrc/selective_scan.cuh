@@ -203,6 +203,7 @@ template <int LPC>
 __device__ __forceinline__ int du_slot(int t, int ch) {
     return group_channels(LPC) == 4 ? ch ^ (((ch >> 4) & 1) | ((t & 1) << 1)) : ch;
 }
+// LPC: the partial sums of a channel
 template <int LPC>
 __device__ __forceinline__ int y_slot(int ch) {
     return group_channels(LPC) == 4 ? ch ^ ((ch >> (LPC == 2 ? 4 : LPC == 4 ? 3 : 2)) & 3) : ch;
@@ -447,135 +448,275 @@ split_kernel(const __grid_constant__ Params p) {
     }
 }
 
-// Backward: the tokens of a sequence in reverse, kSub at a time.  From the stored state
-// before a sub-chunk, its decays a and decayed states q = a h_{t-1} are formed again and
-// kept in registers (h_t = q + delta x B); then, with g the state's gradient,
+// Backward: the tokens of a sequence in reverse, in the forward's tiles and phases, kSub
+// tokens of the lanes' walk at a time.  From the stored state before those, their decays a
+// and decayed states q = a h_{t-1} are formed again and kept in registers (h_t = q + delta x
+// B); then, with g the state's gradient,
 //   dy = dout silu(z),  dz = dout y silu'(z),  g += C dy,
 //   dC = sum_c h dy,  dB = sum_c g delta x,  du = sum_n g B,
 //   ddelta = sum_n g q A + du x,  dA_log = A sum g q delta,
 //   dx = du delta + D dy,  ddt = ddelta sigmoid(dt + dt_bias),  g <- a g.
-// Sums over a channel's entries go over its lanes; dB and dC are summed over the block's
-// channels and leave one row per channel block.
-template <typename T, int LPC>
+// y, du and ddelta's first part are summed over a channel's lanes by the preparers.  dB and
+// dC are summed over a warp's channels by halving shuffles, over the block's warps through
+// shared memory, and leave one row per channel block.
+constexpr int kWarps = kThreads / 32;
+
+template <int LPC>
+struct BwdSmem {
+    static constexpr int N = 4 * LPC, CB = kThreads / LPC, TT = tile_tokens(LPC), YL = LPC < 4 ? LPC : 4;
+    float2 du[TT][CB];                       // delta, delta x
+    alignas(16) float dy[TT][CB];
+    alignas(16) float bc[2][TT][N];
+    alignas(16) float part[3][TT][CB][YL];   // partial sums of y, du and sum_n g q A
+    alignas(16) float dbc[kWarps][TT][2][N];
+};
+
+// Sums 8 values over the 32 / LPC lanes that differ in the lane's channel.  Each shuffle
+// halves the values that a lane still holds; it ends with kKept of them, from at() on.
+template <int LPC>
+struct ChannelSum {
+    static constexpr int M = 32 / LPC;
+    static constexpr int kKept = M >= 8 ? 1 : 8 / M;
+    static __device__ __forceinline__ int at(int lane) { return M >= 8 ? (lane / LPC) / (M / 8) : (lane / LPC) * kKept; }
+    static __device__ __forceinline__ void run(float (&v)[8], int lane) {
+        int nv = 8;
+#pragma unroll
+        for (int o = M / 2; o > 0; o /= 2) {
+            if (nv > 1) {
+                nv /= 2;
+                const bool up = lane & (o * LPC);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < nv) {
+                        const float keep = up ? v[i + nv] : v[i], send = up ? v[i] : v[i + nv];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * LPC);
+                    }
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * LPC);
+            }
+        }
+    }
+};
+
+template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 bwd_kernel(const __grid_constant__ Params p) {
-    constexpr int N = LPC * 4, WARPS = kThreads / 32;
-    __shared__ float bc[WARPS][kSub][2][N];
+    constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E, YL = BwdSmem<LPC>::YL, SUBS = TT / kSub;
+    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;
+    extern __shared__ __align__(16) char smem_raw[];
+    BwdSmem<LPC>& sm = *reinterpret_cast<BwdSmem<LPC>*>(smem_raw);
     const Place<LPC> at(p);
-    const int n = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long s, e;
     if (!p.seq.bounds(n, s, e)) return;   // reported by the first sweep
     const long tokens = p.seq.tokens();
-    float A2[4], g[4] = {0.f, 0.f, 0.f, 0.f};
-    load_v<4>(p.A_log + (long)at.c * N + at.n0, A2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = -expf(A2[i]) * kLog2e;
     const long hrow = ((long)n * p.C + at.c) * N + at.n0;
-    if (p.dh_final && at.on) load_v<4>(p.dh_final + hrow, g);
-    const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f;
-    const float D = p.D ? p.D[at.c] : 0.f;
-    const T* Bm = static_cast<const T*>(p.Bm) + (long)at.g * N + at.n0;
-    const T* Cm = static_cast<const T*>(p.Cm) + (long)at.g * N + at.n0;
-    double dA[4] = {0.0, 0.0, 0.0, 0.0}, dD = 0.0, dbias = 0.0;
-    for (long k = (e - s + kSub - 1) / kSub - 1; k >= 0; --k) {
-        const long t0 = s + k * kSub;
-        const int len = (int)min((long)kSub, e - t0);
-        float a[kSub][4], q[kSub][4], dl[kSub], xs[kSub], dyv[kSub], zv[kSub], yv[kSub], dov[kSub];
-        float h[4];
-        load_v<4>(p.ckpt + (ckpt_slot(s, n, k) * p.C + at.c) * N + at.n0, h);
+    Pair A2[2], g[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    load_decays<LPC>(p, at, A2);
+    if (p.dh_final && at.on) load_pairs<4>(p.dh_final + hrow, g);
+    float bias[E], D[E];
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) {
-            const bool live = at.on && j < len;
-            const long o = (t0 + j) * p.C + at.c;
-            xs[j] = live ? to_f(static_cast<const T*>(p.x)[o]) : 0.f;
-            dl[j] = live ? softplus(to_f(static_cast<const T*>(p.dt)[o]) + bias) : 0.f;
-            dov[j] = live ? to_f(static_cast<const T*>(p.dout)[o]) : 0.f;
-            zv[j] = live && p.z ? to_f(static_cast<const T*>(p.z)[o]) : 0.f;
-            dyv[j] = p.z ? dov[j] * silu(zv[j]) : dov[j];
-            const float u = dl[j] * xs[j];
-            float b[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f}, y = 0.f;
-            if (j < len) {
-                load_v<4>(Bm + (t0 + j) * p.G * N, b);
-                load_v<4>(Cm + (t0 + j) * p.G * N, c);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[j][i] = exp2_fast(dl[j] * A2[i]);
-                q[j][i] = a[j][i] * h[i];
-                h[i] = fmaf(u, b[i], q[j][i]);
-                y = fmaf(h[i], c[i], y);
-            }
-            yv[j] = lanes_sum<LPC>(y);
-        }
-        float dAk[4] = {0.f, 0.f, 0.f, 0.f}, dDk = 0.f, dbk = 0.f;
-#pragma unroll
-        for (int j = kSub - 1; j >= 0; --j) {
-            const bool live = at.on && j < len;
-            const float u = dl[j] * xs[j];
-            float b[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f}, db[4], dc[4], du = 0.f, dd = 0.f;
-            if (j < len) {
-                load_v<4>(Bm + (t0 + j) * p.G * N, b);
-                load_v<4>(Cm + (t0 + j) * p.G * N, c);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ht = fmaf(u, b[i], q[j][i]);
-                g[i] = fmaf(c[i], dyv[j], g[i]);
-                dc[i] = ht * dyv[j];
-                db[i] = g[i] * u;
-                du = fmaf(g[i], b[i], du);
-                const float gq = g[i] * q[j][i];
-                dd = fmaf(gq, A2[i], dd);
-                dAk[i] = fmaf(gq, dl[j], dAk[i]);
-                g[i] *= a[j][i];
-            }
-            du = lanes_sum<LPC>(du);
-            dd = lanes_sum<LPC>(dd) * (1.f / kLog2e);
-            if (live && at.n0 == 0) {
-                const long o = (t0 + j) * p.C + at.c;
-                const float ddelta = fmaf(du, xs[j], dd);
-                const float dv = ddelta * sigmoid(to_f(static_cast<const T*>(p.dt)[o]) + bias);
-                static_cast<T*>(p.dx)[o] = from_f<T>(fmaf(du, dl[j], D * dyv[j]));
-                static_cast<T*>(p.ddt)[o] = from_f<T>(dv);
-                if (p.dz) static_cast<T*>(p.dz)[o] = from_f<T>(dov[j] * fmaf(D, xs[j], yv[j]) * dsilu(zv[j]));
-                dDk = fmaf(dyv[j], xs[j], dDk);
-                dbk += dv;
-            }
-            // over the warp's channels
-#pragma unroll
-            for (int o = LPC; o < 32; o *= 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
-                    dc[i] += __shfl_xor_sync(0xffffffffu, dc[i], o);
-                }
-            if (lane < LPC)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bc[warp][j][0][at.n0 + i] = db[i];
-                    bc[warp][j][1][at.n0 + i] = dc[i];
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dA[i] += (double)dAk[i];
-        dD += (double)dDk;
-        dbias += (double)dbk;
-        __syncthreads();
-        for (int i = threadIdx.x; i < len * 2 * N; i += kThreads) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) v += (&bc[w][0][0][0])[i];
-            p.part_bc[((long)blockIdx.x * tokens + t0) * 2 * N + i] = v;
-        }
-        __syncthreads();
+    for (int i = 0; i < E; ++i) {
+        bias[i] = p.dt_bias && i < at.count ? p.dt_bias[at.gc + i] : 0.f;
+        D[i] = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
     }
+    double dA[4] = {0.0, 0.0, 0.0, 0.0}, dD[E], dbias[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) dD[i] = dbias[i] = 0.0;
+
+    Group<T, E> xr, dr, zr, orr;
+    typename Raw4<T>::type br[QP];
+    Pair hr[SUBS][2];
+    auto fetch = [&](long t0) {
+        const long o = min(t0 + at.gt, e - 1) * p.C + at.gc;
+        xr = load_group<VEC, T, E>(p.x, o, at.count);
+        dr = load_group<VEC, T, E>(p.dt, o, at.count);
+        zr = load_group<VEC, T, E>(p.z ? p.z : p.x, o, at.count);
+        orr = load_group<VEC, T, E>(p.dout, o, at.count);
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = tid + k * kThreads, r = q % QUADS;
+            const long tb = min(t0 + r / (N / 4), e - 1);
+            br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
+                static_cast<const T*>(q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < SUBS; ++k) {   // past the end: the last sub-chunk's, not used
+            const long sub = min((t0 - s) / kSub + k, (e - 1 - s) / kSub);
+            load_pairs<4>(p.ckpt + (ckpt_slot(s, n, sub) * p.C + at.c) * N + at.n0, hr[k]);
+        }
+    };
+    if (s < e) fetch(s + (e - s - 1) / TT * TT);
+    for (long t0 = s + (e - s - 1) / TT * TT; t0 >= s && s < e; t0 -= TT) {
+        const bool live = t0 + at.gt < e && at.count > 0;
+        const Group<T, E> x = xr, dt = dr, z = zr, dout = orr;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            // past the end, and for channels that do not exist: nothing reaches g or a sum
+            const bool in = live && i < at.count;
+            const float delta = in ? softplus(to_f(dt.v[i]) + bias[i]) : 0.f;
+            const float o = in ? to_f(dout.v[i]) : 0.f;
+            sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)] = make_float2(delta, in ? delta * to_f(x.v[i]) : 0.f);
+            sm.dy[at.gt][at.gi + i] = p.z && in ? o * silu(to_f(z.v[i])) : o;
+        }
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = tid + k * kThreads;
+            float v[4];
+            widen(br[k], v);
+            const bool in = t0 + q % QUADS / (N / 4) < e;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
+            if (q < 2 * QUADS) store_v<4>(&sm.bc[0][0][0] + q * 4, v);
+        }
+        Pair h0[SUBS][2];
+#pragma unroll
+        for (int k = 0; k < SUBS; ++k) {
+            h0[k][0] = hr[k][0];
+            h0[k][1] = hr[k][1];
+        }
+        __syncthreads();
+        if (t0 > s) fetch(t0 - TT);
+#pragma unroll
+        for (int k = SUBS - 1; k >= 0; --k) {
+            Pair a[kSub][2], q[kSub][2], dAk[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            Pair h[2] = {h0[k][0], h0[k][1]};
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                const float2 du = sm.du[k * kSub + j][du_slot<LPC>(j, at.li)];
+                Pair b[2];
+                load_pairs<4>(&sm.bc[0][k * kSub + j][at.n0], b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    a[j][i] = exp2_pair(mul2(pair(du.x, du.x), A2[i]));
+                    q[j][i] = mul2(a[j][i], h[i]);
+                    h[i] = fma2(pair(du.y, du.y), b[i], q[j][i]);
+                }
+            }
+#pragma unroll
+            for (int j0 = kSub - kBatch; j0 >= 0; j0 -= kBatch) {
+                float2 du[kBatch];
+                float dy[kBatch], sums[3][kBatch], dbc[kBatch][ChannelSum<LPC>::kKept];
+                Pair b[kBatch][2], c[kBatch][2];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int t = k * kSub + j0 + j;
+                    du[j] = sm.du[t][du_slot<LPC>(t, at.li)];
+                    dy[j] = sm.dy[t][at.li];
+                    load_pairs<4>(&sm.bc[0][t][at.n0], b[j]);
+                    load_pairs<4>(&sm.bc[1][t][at.n0], c[j]);
+                }
+#pragma unroll
+                for (int j = kBatch - 1; j >= 0; --j) {
+                    const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y), dd = pair(dy[j], dy[j]);
+                    Pair y, gb, gqa;
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const Pair qq = q[j0 + j][i], ht = fma2(u, b[j][i], qq);
+                        g[i] = fma2(c[j][i], dd, g[i]);
+                        const Pair gq = mul2(g[i], qq);
+                        y = i ? fma2(ht, c[j][i], y) : mul2(ht, c[j][i]);
+                        gb = i ? fma2(g[i], b[j][i], gb) : mul2(g[i], b[j][i]);
+                        gqa = i ? fma2(gq, A2[i], gqa) : mul2(gq, A2[i]);
+                        dAk[i] = fma2(gq, dl, dAk[i]);
+                        unpair(mul2(g[i], u), v[2 * i], v[2 * i + 1]);
+                        unpair(mul2(ht, dd), v[4 + 2 * i], v[5 + 2 * i]);
+                        g[i] = mul2(a[j0 + j][i], g[i]);
+                    }
+                    float lo, hi;
+                    unpair(y, lo, hi);
+                    sums[0][j] = lo + hi;
+                    unpair(gb, lo, hi);
+                    sums[1][j] = lo + hi;
+                    unpair(gqa, lo, hi);
+                    sums[2][j] = lo + hi;
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+#pragma unroll
+                        for (int o = LPC / YL / 2; o > 0; o /= 2) sums[m][j] += __shfl_xor_sync(0xffffffffu, sums[m][j], o);
+                    ChannelSum<LPC>::run(v, lane);
+#pragma unroll
+                    for (int i = 0; i < ChannelSum<LPC>::kKept; ++i) dbc[j][i] = v[i];
+                }
+                const int ys = y_slot<YL>(at.li), vi = ChannelSum<LPC>::at(lane);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int t = k * kSub + j0 + j;
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) sm.part[m][t][ys][tid % LPC / (LPC / YL)] = sums[m][j];
+#pragma unroll
+                    for (int i = 0; i < ChannelSum<LPC>::kKept; ++i)
+                        sm.dbc[warp][t][(vi + i) >> 2][at.n0 + ((vi + i) & 3)] = dbc[j][i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float lo, hi;
+                unpair(dAk[i], lo, hi);
+                dA[2 * i] += (double)lo;
+                dA[2 * i + 1] += (double)hi;
+            }
+        }
+        __syncthreads();
+        if (live) {
+            const long o = (t0 + at.gt) * p.C + at.gc;
+            float dx[E], ddt[E], dz[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                float sum[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) {
+                    const float* l = sm.part[m][at.gt][y_slot<YL>(at.gi + i)];
+                    sum[m] = l[0] + l[1];
+                    if (YL == 4) sum[m] += l[2] + l[3];
+                }
+                const float xv = to_f(x.v[i]), v = to_f(dt.v[i]) + bias[i], zv = to_f(z.v[i]), ov = to_f(dout.v[i]);
+                const float sg = sigmoid(zv), dy = p.z ? ov * zv * sg : ov;
+                const float ddelta = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e));
+                const bool in = i < at.count;
+                dx[i] = fmaf(sum[1], softplus(v), D[i] * dy);
+                ddt[i] = ddelta * sigmoid(v);
+                dz[i] = ov * fmaf(D[i], xv, sum[0]) * (sg * (1.f + zv * (1.f - sg)));
+                dD[i] += in ? (double)(dy * xv) : 0.0;
+                dbias[i] += in ? (double)ddt[i] : 0.0;
+            }
+            store_group<VEC, T, E>(p.dx, o, dx, at.count);
+            store_group<VEC, T, E>(p.ddt, o, ddt, at.count);
+            if (p.z) store_group<VEC, T, E>(p.dz, o, dz, at.count);
+        }
+        for (int i = tid; i < TT * 2 * N / 4; i += kThreads) {
+            if (t0 + i / (2 * N / 4) >= e) continue;
+            float4 v = reinterpret_cast<const float4*>(&sm.dbc[0][0][0][0])[i];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 o = reinterpret_cast<const float4*>(&sm.dbc[w][0][0][0])[i];
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+            }
+            reinterpret_cast<float4*>(p.part_bc + ((long)blockIdx.x * tokens + t0) * 2 * N)[i] = v;
+        }
+    }
+    // the block's preparers' sums of a channel: over the tile's tokens
+    __syncthreads();
+    double* ds = reinterpret_cast<double*>(smem_raw);   // [TT][CB][2]
+    static_assert(sizeof(BwdSmem<LPC>) >= sizeof(double) * TT * (kThreads / LPC) * 2, "the sums reuse the tile's memory");
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        ds[(at.gt * (kThreads / LPC) + at.gi + i) * 2] = dD[i];
+        ds[(at.gt * (kThreads / LPC) + at.gi + i) * 2 + 1] = dbias[i];
+    }
+    __syncthreads();
     if (!at.on) return;
-    if (p.dh0) store_v<4>(p.dh0 + hrow, g);
+    if (p.dh0) store_pairs<4>(p.dh0 + hrow, g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) p.part_a[hrow + i] = dA[i];
     if (at.n0 == 0) {
-        p.part_d[((long)n * 2) * p.C + at.c] = dD;
-        p.part_d[((long)n * 2 + 1) * p.C + at.c] = dbias;
+        double sum[2] = {0.0, 0.0};
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) sum[m] += ds[(t * (kThreads / LPC) + at.li) * 2 + m];
+        p.part_d[((long)n * 2) * p.C + at.c] = sum[0];
+        p.part_d[((long)n * 2 + 1) * p.C + at.c] = sum[1];
     }
 }
 
