@@ -460,6 +460,7 @@ split_kernel(const __grid_constant__ Params p) {
 // dC are summed over a warp's channels by halving shuffles, over the block's warps through
 // shared memory, and leave one row per channel block.
 constexpr int kWarps = kThreads / 32;
+constexpr int kFlush = 16;
 
 template <int LPC>
 struct BwdSmem {
@@ -469,6 +470,7 @@ struct BwdSmem {
     alignas(16) float bc[2][TT][N];
     alignas(16) float part[3][TT][CB][YL];   // partial sums of y, du and sum_n g q A
     alignas(16) float dbc[kWarps][TT][2][N];
+    double dd[TT][CB][2];                    // sums of dD and ddt_bias, of each preparer
 };
 
 // Sums 8 values over the 32 / LPC lanes that differ in the lane's channel.  Each shuffle
@@ -499,7 +501,7 @@ struct ChannelSum {
 };
 
 template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 bwd_kernel(const __grid_constant__ Params p) {
     constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E, YL = BwdSmem<LPC>::YL, SUBS = TT / kSub;
     constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;
@@ -514,19 +516,29 @@ bwd_kernel(const __grid_constant__ Params p) {
     Pair A2[2], g[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
     load_decays<LPC>(p, at, A2);
     if (p.dh_final && at.on) load_pairs<4>(p.dh_final + hrow, g);
-    float bias[E], D[E];
+    float bias[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         bias[i] = p.dt_bias && i < at.count ? p.dt_bias[at.gc + i] : 0.f;
-        D[i] = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
+        sm.dd[at.gt][at.gi + i][0] = sm.dd[at.gt][at.gi + i][1] = 0.0;
     }
-    double dA[4] = {0.0, 0.0, 0.0, 0.0}, dD[E], dbias[E];
+    // long sums: in fp32 over kSub tokens (dA) or kFlush tiles (dD, ddt_bias), then in fp64
+    double dA[4] = {0.0, 0.0, 0.0, 0.0};
+    float dD[E], dbias[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) dD[i] = dbias[i] = 0.0;
+    for (int i = 0; i < E; ++i) dD[i] = dbias[i] = 0.f;
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            sm.dd[at.gt][at.gi + i][0] += (double)dD[i];
+            sm.dd[at.gt][at.gi + i][1] += (double)dbias[i];
+            dD[i] = dbias[i] = 0.f;
+        }
+    };
+    int since = 0;
 
     Group<T, E> xr, dr, zr, orr;
     typename Raw4<T>::type br[QP];
-    Pair hr[SUBS][2];
     auto fetch = [&](long t0) {
         const long o = min(t0 + at.gt, e - 1) * p.C + at.gc;
         xr = load_group<VEC, T, E>(p.x, o, at.count);
@@ -540,13 +552,15 @@ bwd_kernel(const __grid_constant__ Params p) {
             br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
                 static_cast<const T*>(q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
         }
-#pragma unroll
-        for (int k = 0; k < SUBS; ++k) {   // past the end: the last sub-chunk's, not used
-            const long sub = min((t0 - s) / kSub + k, (e - 1 - s) / kSub);
-            load_pairs<4>(p.ckpt + (ckpt_slot(s, n, sub) * p.C + at.c) * N + at.n0, hr[k]);
-        }
     };
-    if (s < e) fetch(s + (e - s - 1) / TT * TT);
+    // the stored state before the sub-chunk in hand, read one sub-chunk ahead
+    Pair next[2];
+    const float* stored = nullptr;
+    if (s < e) {
+        fetch(s + (e - s - 1) / TT * TT);
+        stored = p.ckpt + (ckpt_slot(s, n, (e - s - 1) / kSub) * p.C + at.c) * N + at.n0;
+        load_pairs<4>(stored, next);
+    }
     for (long t0 = s + (e - s - 1) / TT * TT; t0 >= s && s < e; t0 -= TT) {
         const bool live = t0 + at.gt < e && at.count > 0;
         const Group<T, E> x = xr, dt = dr, z = zr, dout = orr;
@@ -569,18 +583,17 @@ bwd_kernel(const __grid_constant__ Params p) {
             for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
             if (q < 2 * QUADS) store_v<4>(&sm.bc[0][0][0] + q * 4, v);
         }
-        Pair h0[SUBS][2];
-#pragma unroll
-        for (int k = 0; k < SUBS; ++k) {
-            h0[k][0] = hr[k][0];
-            h0[k][1] = hr[k][1];
-        }
         __syncthreads();
         if (t0 > s) fetch(t0 - TT);
-#pragma unroll
+#pragma unroll 1
         for (int k = SUBS - 1; k >= 0; --k) {
+            if (t0 + k * kSub >= e) continue;
             Pair a[kSub][2], q[kSub][2], dAk[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-            Pair h[2] = {h0[k][0], h0[k][1]};
+            Pair h[2] = {next[0], next[1]};
+            if (t0 + k * kSub > s) {
+                stored -= (long)p.C * N;
+                load_pairs<4>(stored, next);
+            }
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 const float2 du = sm.du[k * kSub + j][du_slot<LPC>(j, at.li)];
@@ -671,19 +684,24 @@ bwd_kernel(const __grid_constant__ Params p) {
                     sum[m] = l[0] + l[1];
                     if (YL == 4) sum[m] += l[2] + l[3];
                 }
-                const float xv = to_f(x.v[i]), v = to_f(dt.v[i]) + bias[i], zv = to_f(z.v[i]), ov = to_f(dout.v[i]);
-                const float sg = sigmoid(zv), dy = p.z ? ov * zv * sg : ov;
-                const float ddelta = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e));
-                const bool in = i < at.count;
-                dx[i] = fmaf(sum[1], softplus(v), D[i] * dy);
-                ddt[i] = ddelta * sigmoid(v);
-                dz[i] = ov * fmaf(D[i], xv, sum[0]) * (sg * (1.f + zv * (1.f - sg)));
-                dD[i] += in ? (double)(dy * xv) : 0.0;
-                dbias[i] += in ? (double)ddt[i] : 0.0;
+                const float xv = to_f(x.v[i]), dy = sm.dy[at.gt][at.gi + i];
+                const float delta = sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)].x;
+                const float D = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
+                dx[i] = fmaf(sum[1], delta, D * dy);
+                ddt[i] = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e)) * sigmoid(to_f(dt.v[i]) + bias[i]);
+                dz[i] = p.z ? to_f(dout.v[i]) * fmaf(D, xv, sum[0]) * dsilu(to_f(z.v[i])) : 0.f;
+                if (i < at.count) {
+                    dD[i] = fmaf(dy, xv, dD[i]);
+                    dbias[i] += ddt[i];
+                }
             }
             store_group<VEC, T, E>(p.dx, o, dx, at.count);
             store_group<VEC, T, E>(p.ddt, o, ddt, at.count);
             if (p.z) store_group<VEC, T, E>(p.dz, o, dz, at.count);
+        }
+        if (++since == kFlush) {
+            flush();
+            since = 0;
         }
         for (int i = tid; i < TT * 2 * N / 4; i += kThreads) {
             if (t0 + i / (2 * N / 4) >= e) continue;
@@ -696,15 +714,7 @@ bwd_kernel(const __grid_constant__ Params p) {
             reinterpret_cast<float4*>(p.part_bc + ((long)blockIdx.x * tokens + t0) * 2 * N)[i] = v;
         }
     }
-    // the block's preparers' sums of a channel: over the tile's tokens
-    __syncthreads();
-    double* ds = reinterpret_cast<double*>(smem_raw);   // [TT][CB][2]
-    static_assert(sizeof(BwdSmem<LPC>) >= sizeof(double) * TT * (kThreads / LPC) * 2, "the sums reuse the tile's memory");
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        ds[(at.gt * (kThreads / LPC) + at.gi + i) * 2] = dD[i];
-        ds[(at.gt * (kThreads / LPC) + at.gi + i) * 2 + 1] = dbias[i];
-    }
+    flush();
     __syncthreads();
     if (!at.on) return;
     if (p.dh0) store_pairs<4>(p.dh0 + hrow, g);
@@ -714,7 +724,7 @@ bwd_kernel(const __grid_constant__ Params p) {
         double sum[2] = {0.0, 0.0};
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) sum[m] += ds[(t * (kThreads / LPC) + at.li) * 2 + m];
+            for (int m = 0; m < 2; ++m) sum[m] += sm.dd[t][at.li][m];
         p.part_d[((long)n * 2) * p.C + at.c] = sum[0];
         p.part_d[((long)n * 2 + 1) * p.C + at.c] = sum[1];
     }
