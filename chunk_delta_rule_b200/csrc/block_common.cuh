@@ -155,19 +155,29 @@ struct Seqs {
     }
 };
 
-// out[c] = sum over rows of part[row][c], in double and in a fixed order: 32 columns by 8
-// row lanes a block.
+// out[k][c] = sum over rows of part[k][row][c] for k = blockIdx.y (where out[k] is given), in
+// double and in a fixed order: 32 columns by 8 row lanes a block.
+struct SumRows {
+    const float* part;
+    float* out[3];
+    long rows, cols;
+};
 __global__ void __launch_bounds__(256)
-sum_rows_kernel(const float* __restrict__ part, float* __restrict__ out, long rows, long cols) {
+sum_rows_kernel(const __grid_constant__ SumRows p) {
     __shared__ double s[8][33];
+    float* out = p.out[blockIdx.y];
+    if (!out) return;
+    const float* part = p.part + blockIdx.y * p.rows * p.cols;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const long c = (long)blockIdx.x * 32 + lane;
     double acc = 0.0;
-    if (c < cols)
-        for (long r = w; r < rows; r += 8) acc += (double)part[r * cols + c];
+    if (c < p.cols) {
+#pragma unroll 8
+        for (long r = w; r < p.rows; r += 8) acc += (double)part[r * p.cols + c];
+    }
     s[w][lane] = acc;
     __syncthreads();
-    if (w == 0 && c < cols) {
+    if (w == 0 && c < p.cols) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) acc += s[i][lane];
         out[c] = (float)acc;

@@ -10,6 +10,8 @@
 // so that any width up to 8192 runs.
 #pragma once
 
+#include <type_traits>
+
 #include "block_common.cuh"
 
 namespace comba {
@@ -18,6 +20,16 @@ namespace norm {
 using namespace blk;
 
 constexpr int kMaxWidth = 8192;
+// Blocks of 256 threads of the backwards that an SM's registers hold: 80 registers a thread,
+// and 128 where three column sums and up to four rows are kept.
+constexpr int kGatedBlocks = 3, kResidualBlocks = 2;
+
+// 8 values of a row as they are stored.
+template <typename T, bool VECTOR>
+struct Raw {
+    static constexpr int PARTS = VECTOR ? (int)(8 * sizeof(T) / 16) : 8;
+    typename std::conditional<VECTOR, uint4, T>::type v[PARTS];
+};
 
 // A thread's 8 columns of its row: consecutive (VECTOR), or tid, tid + TPR, ...
 template <bool VECTOR>
@@ -25,16 +37,29 @@ struct Cols {
     int tid, tpr, D;
     __device__ __forceinline__ bool on(int i) const { return VECTOR ? tid * 8 < D : tid + i * tpr < D; }
     __device__ __forceinline__ int at(int i) const { return VECTOR ? tid * 8 + i : tid + i * tpr; }
+    // Loads carry no condition, so that they stay in flight until widen() needs them: columns
+    // past the row's end read its first one.
     template <typename T>
-    __device__ __forceinline__ void load(const T* __restrict__ row, float (&v)[8]) const {
+    __device__ __forceinline__ Raw<T, VECTOR> fetch(const void* base, long row) const {
+        const T* p = static_cast<const T*>(base) + row * D;
+        Raw<T, VECTOR> r;
         if constexpr (VECTOR) {
-            if (tid * 8 < D) load_v<8>(row + tid * 8, v);
-            else
+            p += on(0) ? tid * 8 : 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            for (int i = 0; i < r.PARTS; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = on(i) ? to_f(row[at(i)]) : 0.f;
+            for (int i = 0; i < 8; ++i) r.v[i] = p[on(i) ? at(i) : 0];
+        }
+        return r;
+    }
+    template <typename T>
+    __device__ __forceinline__ void widen(const Raw<T, VECTOR>& r, float (&v)[8]) const {
+        if constexpr (VECTOR) {   // all on or all off: row_sum leaves off threads out
+            load_v<8>(reinterpret_cast<const T*>(r.v), v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = on(i) ? to_f(r.v[i]) : 0.f;
         }
     }
     template <typename T>
@@ -50,8 +75,7 @@ struct Cols {
     // A row of parameters; `other` where there is none.
     __device__ __forceinline__ void param(const float* __restrict__ p, float other, float (&v)[8]) const {
         if (p) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = on(i) ? p[at(i)] : 0.f;
+            widen<float>(fetch<float>(p, 0), v);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = other;
@@ -59,13 +83,15 @@ struct Cols {
     }
 };
 
-// Sums of K values over the TPR threads of a row, to all of them.  Up to 32 threads: by
+// Sums of K values over the TPR threads of a row (those with columns on), to all of them.  Up to 32 threads: by
 // shuffles in their part of the warp.  More: the block is one row, and the warps' sums
 // go through shared memory; `slot` alternates between two buffers, so that one barrier
 // a call is enough.
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*buf)[32][K], int slot) {
-    const int width = tpr < 32 ? tpr : 32;
+template <int K, bool VECTOR>
+__device__ __forceinline__ void row_sum(const Cols<VECTOR>& cols, float (&v)[K], float (*buf)[32][K], int slot) {
+    const int tpr = cols.tpr, width = tpr < 32 ? tpr : 32;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = cols.on(0) ? v[k] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         if (o < width)
@@ -78,14 +104,16 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*buf)[32]
         for (int k = 0; k < K; ++k) buf[slot][warp][k] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < warps ? buf[slot][lane][k] : 0.f;
+    for (int k = 0; k < K; ++k) v[k] = buf[slot][lane & (warps - 1)][k];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
+        if (o < warps)
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
 
-__device__ __forceinline__ float inv_rms(float sq, int D, float eps) { return 1.f / sqrtf(sq / (float)D + eps); }
+// 1 / sqrt(mean + eps) of a sum of squares, from the hardware's approximation (2 ulp).
+__device__ __forceinline__ float inv_rms(float sq, float inv_d, float eps) { return rsqrtf(fmaf(sq, inv_d, eps)); }
 
 // ------------------------------------------------------------------ gated norm
 struct Gated {
@@ -95,11 +123,13 @@ struct Gated {
     float* part;       // backward: [blocks, D] partial sums of dweight
     long rows;
     int D, tpr;
-    float eps;
+    float eps, inv_d;
 };
 
-template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(1024)
+// Blocks walk their rows with the next one's loads in flight.  MAXT: the largest block; up
+// to 512 threads have the registers to keep the parameters over the rows.
+template <typename T, bool VECTOR, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1)
 gated_fwd_kernel(const __grid_constant__ Gated p) {
     __shared__ float buf[2][32][1];
     const int per = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
@@ -107,16 +137,24 @@ gated_fwd_kernel(const __grid_constant__ Gated p) {
     float w[8];
     cols.param(p.weight, 1.f, w);
     int slot = 0;
-    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += (long)gridDim.x * per, slot ^= 1) {
+    const long step = (long)gridDim.x * per;
+    long row = min((long)blockIdx.x * per + sub, p.rows - 1);
+    Raw<T, VECTOR> xr = cols.template fetch<T>(p.x, row), gr = cols.template fetch<T>(p.gate, row);
+    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += step, slot ^= 1) {
+        const long at = row * p.D;
         const bool live = r0 + sub < p.rows;
-        const long at = (live ? r0 + sub : p.rows - 1) * p.D;
         float x[8], g[8], sq[1] = {0.f};
-        cols.load(static_cast<const T*>(p.x) + at, x);
-        cols.load(static_cast<const T*>(p.gate) + at, g);
+        cols.template widen<T>(xr, x);
+        cols.template widen<T>(gr, g);
+        row = min(r0 + step + sub, p.rows - 1);
+        if (r0 + step < p.rows) {
+            xr = cols.template fetch<T>(p.x, row);
+            gr = cols.template fetch<T>(p.gate, row);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sq[0] = fmaf(x[i], x[i], sq[0]);
-        row_sum<1>(sq, p.tpr, buf, slot);
-        const float r = inv_rms(sq[0], p.D, p.eps);
+        row_sum<1>(cols, sq, buf, slot);
+        const float r = inv_rms(sq[0], p.inv_d, p.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i] * silu(g[i]);
         if (live) cols.store(static_cast<T*>(p.out) + at, x);
@@ -147,8 +185,8 @@ __device__ __forceinline__ void column_sums(const Cols<VECTOR>& cols, float (&ac
 // Backward.  With n = x r, s = silu(gate), q = dout w s:
 //   dx = r (q - n mean(q n)),  dgate = dout n w silu'(gate),  dweight = sum over rows dout n s.
 // Both row sums, of x^2 and q x, are taken at once.
-template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(1024)
+template <typename T, bool VECTOR, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? kGatedBlocks : 1)
 gated_bwd_kernel(const __grid_constant__ Gated p) {
     __shared__ float buf[2][32][2];
     extern __shared__ float smem[];
@@ -159,22 +197,32 @@ gated_bwd_kernel(const __grid_constant__ Gated p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[0][i] = 0.f;
     int slot = 0;
-    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += (long)gridDim.x * per, slot ^= 1) {
+    const long step = (long)gridDim.x * per;
+    long row = min((long)blockIdx.x * per + sub, p.rows - 1);
+    Raw<T, VECTOR> xr = cols.template fetch<T>(p.x, row), gr = cols.template fetch<T>(p.gate, row),
+                   dr = cols.template fetch<T>(p.dout, row);
+    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += step, slot ^= 1) {
+        const long at = row * p.D;
         const bool live = r0 + sub < p.rows;
-        const long at = (live ? r0 + sub : p.rows - 1) * p.D;
         float x[8], g[8], d[8], s[8], sum[2] = {0.f, 0.f};
-        cols.load(static_cast<const T*>(p.x) + at, x);
-        cols.load(static_cast<const T*>(p.gate) + at, g);
-        cols.load(static_cast<const T*>(p.dout) + at, d);
+        cols.template widen<T>(xr, x);
+        cols.template widen<T>(gr, g);
+        cols.template widen<T>(dr, d);
+        row = min(r0 + step + sub, p.rows - 1);
+        if (r0 + step < p.rows) {
+            xr = cols.template fetch<T>(p.x, row);
+            gr = cols.template fetch<T>(p.gate, row);
+            dr = cols.template fetch<T>(p.dout, row);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s[i] = sigmoid(g[i]);
             sum[0] = fmaf(x[i], x[i], sum[0]);
             sum[1] = fmaf(d[i] * w[i] * g[i] * s[i], x[i], sum[1]);
         }
-        row_sum<2>(sum, p.tpr, buf, slot);
-        const float r = inv_rms(sum[0], p.D, p.eps);
-        const float mean = sum[1] * r / (float)p.D;   // mean(q n)
+        row_sum<2>(cols, sum, buf, slot);
+        const float r = inv_rms(sum[0], p.inv_d, p.eps);
+        const float mean = sum[1] * r * p.inv_d;   // mean(q n)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float n = x[i] * r, act = g[i] * s[i], dn = d[i] * n;
@@ -198,48 +246,58 @@ struct Residual {
     float* part;       // backward: [3, blocks, D] partial sums of dweight, dscale, dpost
     long rows;
     int D, tpr;
-    float eps;
+    float eps, inv_d;
 };
 
 // T: block output, its norm and their cotangents; TR: the residual stream.
-template <typename T, typename TR, bool VECTOR, bool POST>
-__global__ void __launch_bounds__(1024)
+template <typename T, typename TR, bool VECTOR, bool POST, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1)
 residual_fwd_kernel(const __grid_constant__ Residual p) {
     __shared__ float buf[2][32][1];
     const int per = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
     const Cols<VECTOR> cols{(int)threadIdx.x % p.tpr, p.tpr, p.D};
+    float w[8], sc[8], po[8];
+    cols.param(p.weight, 1.f, w);
+    cols.param(p.scale, 1.f, sc);
+    if (POST) cols.param(p.post, 1.f, po);
     int slot = 0;
-    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += (long)gridDim.x * per) {
+    const long step = (long)gridDim.x * per;
+    long row = min((long)blockIdx.x * per + sub, p.rows - 1);
+    Raw<T, VECTOR> xr = cols.template fetch<T>(p.x, row);
+    Raw<TR, VECTOR> hr = cols.template fetch<TR>(p.residual, row);
+    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += step) {
+        const long at = row * p.D;
         const bool live = r0 + sub < p.rows;
-        const long at = (live ? r0 + sub : p.rows - 1) * p.D;
-        float x[8], h[8], a[8], sq[1] = {0.f};
-        cols.load(static_cast<const T*>(p.x) + at, x);
-        cols.load(static_cast<const TR*>(p.residual) + at, h);
+        float x[8], h[8], sq[1] = {0.f};
+        cols.template widen<T>(xr, x);
+        cols.template widen<TR>(hr, h);
+        row = min(r0 + step + sub, p.rows - 1);
+        if (r0 + step < p.rows) {
+            xr = cols.template fetch<T>(p.x, row);
+            hr = cols.template fetch<TR>(p.residual, row);
+        }
         if (POST) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sq[0] = fmaf(x[i], x[i], sq[0]);
-            row_sum<1>(sq, p.tpr, buf, slot);
+            row_sum<1>(cols, sq, buf, slot);
             slot ^= 1;
-            const float r = inv_rms(sq[0], p.D, p.eps);
-            cols.param(p.post, 1.f, a);
+            const float r = inv_rms(sq[0], p.inv_d, p.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * a[i];
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * po[i];
             sq[0] = 0.f;
         }
-        cols.param(p.scale, 1.f, a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             // the norm reads the stream as it is stored, which is what the backward sees
-            h[i] = to_f(from_f<TR>(fmaf(x[i], a[i], h[i])));
+            h[i] = to_f(from_f<TR>(fmaf(x[i], sc[i], h[i])));
             sq[0] = fmaf(h[i], h[i], sq[0]);
         }
         if (live) cols.store(static_cast<TR*>(p.h) + at, h);
-        row_sum<1>(sq, p.tpr, buf, slot);
+        row_sum<1>(cols, sq, buf, slot);
         slot ^= 1;
-        const float r = inv_rms(sq[0], p.D, p.eps);
-        cols.param(p.weight, 1.f, a);
+        const float r = inv_rms(sq[0], p.inv_d, p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = h[i] * r * a[i];
+        for (int i = 0; i < 8; ++i) h[i] = h[i] * r * w[i];
         if (live) cols.store(static_cast<T*>(p.out) + at, h);
     }
 }
@@ -249,47 +307,58 @@ residual_fwd_kernel(const __grid_constant__ Residual p) {
 //   dscale = sum tot u,  du = scale tot,
 //   dx = du, or with n = x r(x), u = n w_post:  r(x) (du w_post - n mean(du w_post n)),
 //   dpost = sum du n.
-template <typename T, typename TR, bool VECTOR, bool POST>
-__global__ void __launch_bounds__(1024)
+template <typename T, typename TR, bool VECTOR, bool POST, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? kResidualBlocks : 1)
 residual_bwd_kernel(const __grid_constant__ Residual p) {
     __shared__ float buf3[2][32][3];
     __shared__ float buf1[2][32][1];
     extern __shared__ float smem[];
     const int per = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
     const Cols<VECTOR> cols{(int)threadIdx.x % p.tpr, p.tpr, p.D};
-    float w[8], sc[8], po[8], acc[3][8];
-    cols.param(p.weight, 1.f, w);
-    cols.param(p.scale, 1.f, sc);
-    cols.param(p.post, 1.f, po);
+    float acc[3][8];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
     int slot = 0;
-    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += (long)gridDim.x * per, slot ^= 1) {
+    const long step = (long)gridDim.x * per;
+    long row = min((long)blockIdx.x * per + sub, p.rows - 1);
+    Raw<T, VECTOR> xr = cols.template fetch<T>(p.x, row), dr = cols.template fetch<T>(p.dy, row);
+    Raw<TR, VECTOR> hr = cols.template fetch<TR>(p.h_in, row), gr = cols.template fetch<TR>(p.dh ? p.dh : p.h_in, row);
+    for (long r0 = (long)blockIdx.x * per; r0 < p.rows; r0 += step, slot ^= 1) {
+        const long at = row * p.D;
         const bool live = r0 + sub < p.rows;
-        const long at = (live ? r0 + sub : p.rows - 1) * p.D;
         float x[8], h[8], d[8], g[8], sum[3] = {0.f, 0.f, 0.f};
-        cols.load(static_cast<const T*>(p.x) + at, x);
-        cols.load(static_cast<const TR*>(p.h_in) + at, h);
-        cols.load(static_cast<const T*>(p.dy) + at, d);
-        if (p.dh) {
-            cols.load(static_cast<const TR*>(p.dh) + at, g);
-        } else {
+        cols.template widen<T>(xr, x);
+        cols.template widen<TR>(hr, h);
+        cols.template widen<T>(dr, d);
+        cols.template widen<TR>(gr, g);
+        row = min(r0 + step + sub, p.rows - 1);
+        if (r0 + step < p.rows) {
+            xr = cols.template fetch<T>(p.x, row);
+            hr = cols.template fetch<TR>(p.h_in, row);
+            dr = cols.template fetch<T>(p.dy, row);
+            gr = cols.template fetch<TR>(p.dh ? p.dh : p.h_in, row);
+        }
+        if (!p.dh)
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = 0.f;
-        }
+        // the parameters come from L1 each time: registers for them would halve the rows in flight
+        float w[8];
+        cols.param(p.weight, 1.f, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             sum[0] = fmaf(h[i], h[i], sum[0]);
             sum[1] = fmaf(d[i] * w[i], h[i], sum[1]);
             if (POST) sum[2] = fmaf(x[i], x[i], sum[2]);
         }
-        row_sum<3>(sum, p.tpr, buf3, slot);
-        const float r = inv_rms(sum[0], p.D, p.eps);
-        const float mean = sum[1] * r / (float)p.D;
-        const float rx = POST ? inv_rms(sum[2], p.D, p.eps) : 1.f;
-        float q[1] = {0.f};
+        row_sum<3>(cols, sum, buf3, slot);
+        const float r = inv_rms(sum[0], p.inv_d, p.eps);
+        const float mean = sum[1] * r * p.inv_d;
+        const float rx = POST ? inv_rms(sum[2], p.inv_d, p.eps) : 1.f;
+        float q[1] = {0.f}, sc[8], po[8];
+        cols.param(p.scale, 1.f, sc);
+        cols.param(POST ? p.post : nullptr, 1.f, po);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float m = h[i] * r, n = x[i] * rx;
@@ -306,8 +375,8 @@ residual_bwd_kernel(const __grid_constant__ Residual p) {
         }
         if (live) cols.store(static_cast<TR*>(p.dres) + at, g);
         if (POST) {
-            row_sum<1>(q, p.tpr, buf1, slot);
-            const float mq = q[0] / (float)p.D;
+            row_sum<1>(cols, q, buf1, slot);
+            const float mq = q[0] * p.inv_d;
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = rx * (d[i] - x[i] * mq);
         }
@@ -324,10 +393,16 @@ inline int row_threads(int D) {
     return t;
 }
 inline int block_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
+// Blocks of the forward: a few for each SM, which walk the rows.
+inline long fwd_blocks(long rows, int tpr) {
+    const int threads = block_threads(tpr);
+    const long want = (long)kSMs * (threads >= 1024 ? 2 : 2048 / threads), need = ceil_div(rows, threads / tpr);
+    return need < want ? need : want;
+}
 // Blocks of the backward: each walks several rows and leaves one row of partial sums.
-inline long bwd_blocks(long rows, int D) {
+inline long bwd_blocks(long rows, int D, int per_sm) {
     const int tpr = row_threads(D), threads = block_threads(tpr);
-    const long want = (long)kSMs * (threads >= 1024 ? 1 : 1024 / threads);
+    const long want = (long)kSMs * (threads <= 256 ? per_sm * 256 / threads : 1);
     const long need = ceil_div(rows, threads / tpr);
     return need < want ? need : want;
 }

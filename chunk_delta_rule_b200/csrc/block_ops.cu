@@ -459,35 +459,53 @@ int norm_sizes(long long rows, int D, int dtype, float eps) {
     return COMBA_OK;
 }
 
-unsigned fwd_blocks(long rows, int per) {
-    const long b = ceil_div(rows, per);
-    return (unsigned)(b < kMaxGrid ? b : kMaxGrid);
+template <typename T, bool VECTOR>
+int gated_fwd(const norm::Gated& p, cudaStream_t s) {
+    const int threads = norm::block_threads(p.tpr);
+    const unsigned blocks = (unsigned)norm::fwd_blocks(p.rows, p.tpr);
+    if (threads <= 512) norm::gated_fwd_kernel<T, VECTOR, 512><<<blocks, threads, 0, s>>>(p);
+    else norm::gated_fwd_kernel<T, VECTOR, 1024><<<blocks, threads, 0, s>>>(p);
+    return launched();
 }
 
 template <typename T, bool VECTOR>
 int gated_bwd(const norm::Gated& p, unsigned blocks, cudaStream_t s) {
     const int threads = norm::block_threads(p.tpr);
     const size_t smem = threads > p.tpr ? (size_t)threads * 8 * sizeof(float) : 0;
-    norm::gated_bwd_kernel<T, VECTOR><<<blocks, threads, smem, s>>>(p);
+    if (threads <= 256) norm::gated_bwd_kernel<T, VECTOR, 256><<<blocks, threads, smem, s>>>(p);
+    else if (threads <= 512) norm::gated_bwd_kernel<T, VECTOR, 512><<<blocks, threads, smem, s>>>(p);
+    else norm::gated_bwd_kernel<T, VECTOR, 1024><<<blocks, threads, smem, s>>>(p);
+    return launched();
+}
+
+template <typename T, typename TR, bool VECTOR, bool POST>
+int residual_fwd_post(const norm::Residual& p, cudaStream_t s) {
+    const int threads = norm::block_threads(p.tpr);
+    const unsigned blocks = (unsigned)norm::fwd_blocks(p.rows, p.tpr);
+    if (threads <= 512) norm::residual_fwd_kernel<T, TR, VECTOR, POST, 512><<<blocks, threads, 0, s>>>(p);
+    else norm::residual_fwd_kernel<T, TR, VECTOR, POST, 1024><<<blocks, threads, 0, s>>>(p);
     return launched();
 }
 
 template <typename T, typename TR, bool VECTOR>
 int residual_fwd(const norm::Residual& p, cudaStream_t s) {
+    return p.post ? residual_fwd_post<T, TR, VECTOR, true>(p, s) : residual_fwd_post<T, TR, VECTOR, false>(p, s);
+}
+
+template <typename T, typename TR, bool VECTOR, bool POST>
+int residual_bwd_post(const norm::Residual& p, unsigned blocks, cudaStream_t s) {
     const int threads = norm::block_threads(p.tpr);
-    const unsigned blocks = fwd_blocks(p.rows, threads / p.tpr);
-    if (p.post) norm::residual_fwd_kernel<T, TR, VECTOR, true><<<blocks, threads, 0, s>>>(p);
-    else norm::residual_fwd_kernel<T, TR, VECTOR, false><<<blocks, threads, 0, s>>>(p);
+    const size_t smem = threads > p.tpr ? (size_t)threads * 8 * sizeof(float) : 0;
+    if (threads <= 256) norm::residual_bwd_kernel<T, TR, VECTOR, POST, 256><<<blocks, threads, smem, s>>>(p);
+    else if (threads <= 512) norm::residual_bwd_kernel<T, TR, VECTOR, POST, 512><<<blocks, threads, smem, s>>>(p);
+    else norm::residual_bwd_kernel<T, TR, VECTOR, POST, 1024><<<blocks, threads, smem, s>>>(p);
     return launched();
 }
 
 template <typename T, typename TR, bool VECTOR>
 int residual_bwd(const norm::Residual& p, unsigned blocks, cudaStream_t s) {
-    const int threads = norm::block_threads(p.tpr);
-    const size_t smem = threads > p.tpr ? (size_t)threads * 8 * sizeof(float) : 0;
-    if (p.post) norm::residual_bwd_kernel<T, TR, VECTOR, true><<<blocks, threads, smem, s>>>(p);
-    else norm::residual_bwd_kernel<T, TR, VECTOR, false><<<blocks, threads, smem, s>>>(p);
-    return launched();
+    return p.post ? residual_bwd_post<T, TR, VECTOR, true>(p, blocks, s)
+                  : residual_bwd_post<T, TR, VECTOR, false>(p, blocks, s);
 }
 
 #define COMBA_RESIDUAL_DISPATCH(f, dtype, rdtype, vec, ...)                                                    \
@@ -508,25 +526,17 @@ extern "C" int comba_gated_norm_fwd(const void* x, const void* gate, const float
     if (!args_ok(ins, outs)) return COMBA_EINVAL;
     norm::Gated p{};
     p.x = x; p.gate = gate; p.weight = weight; p.out = out;
-    p.rows = rows; p.D = D; p.eps = eps;
+    p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
-    const int threads = norm::block_threads(p.tpr);
-    const unsigned blocks = fwd_blocks(rows, threads / p.tpr);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, gate, out});
-    if (dtype == COMBA_BF16) {
-        if (vec) norm::gated_fwd_kernel<bf16, true><<<blocks, threads, 0, s>>>(p);
-        else norm::gated_fwd_kernel<bf16, false><<<blocks, threads, 0, s>>>(p);
-    } else {
-        if (vec) norm::gated_fwd_kernel<float, true><<<blocks, threads, 0, s>>>(p);
-        else norm::gated_fwd_kernel<float, false><<<blocks, threads, 0, s>>>(p);
-    }
-    return launched();
+    const bool vec = vector_rows(D, {x, gate, weight, out});
+    if (dtype == COMBA_BF16) return vec ? gated_fwd<bf16, true>(p, s) : gated_fwd<bf16, false>(p, s);
+    return vec ? gated_fwd<float, true>(p, s) : gated_fwd<float, false>(p, s);
 }
 
 extern "C" size_t comba_gated_norm_bwd_workspace_size(long long rows, int D) {
     if (rows <= 0 || D <= 0 || D > norm::kMaxWidth) return 0;
-    return (size_t)norm::bwd_blocks(rows, D) * D * sizeof(float);
+    return (size_t)norm::bwd_blocks(rows, D, norm::kGatedBlocks) * D * sizeof(float);
 }
 
 extern "C" int comba_gated_norm_bwd(const void* x, const void* gate, const float* weight, const void* dout, void* dx,
@@ -543,17 +553,17 @@ extern "C" int comba_gated_norm_bwd(const void* x, const void* gate, const float
     norm::Gated p{};
     p.x = x; p.gate = gate; p.weight = weight; p.dout = dout; p.dx = dx; p.dgate = dgate;
     p.part = static_cast<float*>(workspace);
-    p.rows = rows; p.D = D; p.eps = eps;
+    p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
-    const long blocks = rows > 0 ? norm::bwd_blocks(rows, D) : 0;
+    const long blocks = rows > 0 ? norm::bwd_blocks(rows, D, norm::kGatedBlocks) : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, gate, dout, dx, dgate});
+    const bool vec = vector_rows(D, {x, gate, weight, dout, dx, dgate});
     if (blocks) {
         const int st = dtype == COMBA_BF16 ? (vec ? gated_bwd<bf16, true>(p, (unsigned)blocks, s) : gated_bwd<bf16, false>(p, (unsigned)blocks, s))
                                            : (vec ? gated_bwd<float, true>(p, (unsigned)blocks, s) : gated_bwd<float, false>(p, (unsigned)blocks, s));
         if (st) return st;
     }
-    sum_rows_kernel<<<(unsigned)ceil_div(D, 32), 256, 0, s>>>(p.part, dweight, blocks, D);
+    sum_rows_kernel<<<(unsigned)ceil_div(D, 32), 256, 0, s>>>(SumRows{p.part, {dweight}, blocks, D});
     return launched();
 }
 
@@ -570,14 +580,15 @@ extern "C" int comba_residual_norm_fwd(const void* x, const void* residual, cons
     if (!args_ok(ins, outs)) return COMBA_EINVAL;
     norm::Residual p{};
     p.x = x; p.residual = residual; p.weight = weight; p.scale = scale; p.post = post_weight; p.out = out; p.h = h;
-    p.rows = rows; p.D = D; p.eps = eps;
+    p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
-    const bool vec = vector_rows(D, {x, residual, out, h});
+    const bool vec = vector_rows(D, {x, residual, weight, scale, post_weight, out, h});
     return COMBA_RESIDUAL_DISPATCH(residual_fwd, dtype, residual_dtype, vec, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t comba_residual_norm_bwd_workspace_size(long long rows, int D) {
-    return 3 * comba_gated_norm_bwd_workspace_size(rows, D);
+    if (rows <= 0 || D <= 0 || D > norm::kMaxWidth) return 0;
+    return 3 * (size_t)norm::bwd_blocks(rows, D, norm::kResidualBlocks) * D * sizeof(float);
 }
 
 extern "C" int comba_residual_norm_bwd(const void* x, const void* h, const float* weight, const float* scale,
@@ -601,16 +612,14 @@ extern "C" int comba_residual_norm_bwd(const void* x, const void* h, const float
     p.x = x; p.h_in = h; p.weight = weight; p.scale = scale; p.post = post_weight; p.dy = dy; p.dh = dh;
     p.dx = dx; p.dres = dresidual;
     p.part = static_cast<float*>(workspace);
-    p.rows = rows; p.D = D; p.eps = eps;
+    p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
-    const long blocks = rows > 0 ? norm::bwd_blocks(rows, D) : 0;
+    const long blocks = rows > 0 ? norm::bwd_blocks(rows, D, norm::kResidualBlocks) : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, h, dy, dh, dx, dresidual});
+    const bool vec = vector_rows(D, {x, h, weight, scale, post_weight, dy, dh, dx, dresidual});
     if (blocks)
         if (int st = COMBA_RESIDUAL_DISPATCH(residual_bwd, dtype, residual_dtype, vec, p, (unsigned)blocks, s)) return st;
-    float* sums[] = {dweight, dscale, dpost_weight};
-    for (int k = 0; k < 3; ++k)
-        if (sums[k])
-            sum_rows_kernel<<<(unsigned)ceil_div(D, 32), 256, 0, s>>>(p.part + (size_t)k * blocks * D, sums[k], blocks, D);
+    sum_rows_kernel<<<dim3((unsigned)ceil_div(D, 32), 3), 256, 0, s>>>(
+        SumRows{p.part, {dweight, dscale, dpost_weight}, blocks, D});
     return launched();
 }

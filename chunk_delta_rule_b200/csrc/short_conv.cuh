@@ -256,8 +256,10 @@ sum_kernel(const float* __restrict__ part, float* __restrict__ dweight, float* _
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
     double acc = 0.0;
-    if (c < C)
+    if (c < C) {
+#pragma unroll 8
         for (long i = r; i < tiles; i += 8) acc += (double)part[(i * (W + 1) + j) * C + c];
+    }
     s[r][lane] = acc;
     __syncthreads();
     if (r != 0 || c >= C) return;

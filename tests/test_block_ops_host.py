@@ -137,6 +137,7 @@ def test_workspace_sizes(lib):
     assert (lib.comba_selective_scan_bwd_workspace_size(2, 4096, 32, 2, 16, 0)
             > lib.comba_selective_scan_bwd_workspace_size(2, 64, 32, 2, 16, 0) > 0)
     assert lib.comba_residual_norm_bwd_workspace_size(100, 64) == 3 * lib.comba_gated_norm_bwd_workspace_size(100, 64) > 0
+    assert lib.comba_residual_norm_bwd_workspace_size(0, 64) == lib.comba_residual_norm_bwd_workspace_size(100, 8193) == 0
 
 
 def test_the_binding_refuses_what_is_not_a_device_tensor():
