@@ -65,6 +65,9 @@ __device__ __forceinline__ void load_v(const float* __restrict__ p, float (&x)[V
     }
 }
 
+// Brings the line at p into L2 while nothing waits for it.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
@@ -94,11 +97,40 @@ __device__ __forceinline__ void store_v(float* __restrict__ p, const float (&x)[
     }
 }
 
-// sigmoid(v) = 1 / (1 + exp(-v)).  The division is exact enough for fp32 outputs; the
-// exponential overflows to inf only where the quotient is 0.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-// Where exp(-v) overflows __fdividef's range (its result is 0 for a divisor above 2^126),
-// 0 is the right value, and v * 0 is (minus) zero for finite v.
+// Pairs of fp32 values in a 64-bit register: one instruction for two products or sums.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 2^v and 1 / v by the hardware's approximations (relative errors 2^-22 and 2^-23).
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// sigmoid(v) = 1 / (1 + exp(-v)); where the exponential overflows, 0.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.f + exp2_fast(-kLog2e * v)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d silu / dv
 __device__ __forceinline__ float dsilu(float v) {
@@ -112,8 +144,8 @@ __device__ __forceinline__ float dsilu(float v) {
 // above, from the hardware's logarithm of 1 + e, whose absolute error of 2^-22 is 6e-7 of
 // results of at least 0.4.
 __device__ __forceinline__ float softplus(float v) {
-    const float e = __expf(v);
-    const float s = __fdividef(e, 2.f + e), q = s * s;
+    const float e = exp2_fast(kLog2e * v);
+    const float s = e * rcp_fast(2.f + e), q = s * s;
     float r = fmaf(q, 1.f / 11.f, 1.f / 9.f);
     r = fmaf(q, r, 1.f / 7.f);
     r = fmaf(q, r, 1.f / 5.f);

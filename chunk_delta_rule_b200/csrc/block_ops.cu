@@ -33,10 +33,11 @@ size_t volume(size_t a, size_t b, size_t c = 1) {
     return ab * c;
 }
 
-bool vector_rows(int C, std::initializer_list<const void*> ptrs) {
-    if (C % kVec) return false;
+// Rows of C elements that start aligned for accesses of `per` elements and hold whole ones.
+bool vector_rows(int C, int per, size_t align, std::initializer_list<const void*> ptrs) {
+    if (C % per) return false;
     for (const void* p : ptrs)
-        if (!aligned(p, 16)) return false;
+        if (!aligned(p, align)) return false;
     return true;
 }
 
@@ -44,7 +45,7 @@ bool vector_rows(int C, std::initializer_list<const void*> ptrs) {
 template <typename T, int W, int V>
 int conv_fwd(conv::Params& p, bool silu, cudaStream_t s) {
     const int cv = p.C / V;
-    p.L = conv::tile_tokens(p.seq.tokens(), cv, 16);
+    p.L = conv::tile_tokens(p.seq.tokens(), cv, 64);
     const long tiles = ceil_div(p.seq.tokens(), p.L);
     const long states = (p.fin || p.seq.cu) ? (long)p.seq.N * (W - 1) : 0;
     const long total = (tiles + states) * cv, blocks = ceil_div(total, conv::kThreads);
@@ -57,19 +58,23 @@ int conv_fwd(conv::Params& p, bool silu, cudaStream_t s) {
 
 // Tiles of the backward, and so the rows of partial sums: the same for either path's
 // vector width, so that the workspace does not depend on pointers.
-int conv_bwd_tile(size_t tokens, int C) { return conv::tile_tokens((long)tokens, (C + kVec - 1) / kVec, 64); }
+int conv_bwd_tile(size_t tokens, int C) { return conv::tile_tokens((long)tokens, (C + conv::kChannels - 1) / conv::kChannels, 128); }
 
 template <typename T, int W, int V>
 int conv_bwd(conv::Params& p, float* dweight, float* dbias, bool silu, cudaStream_t s) {
     const int cv = p.C / V;
     p.L = conv_bwd_tile((size_t)p.seq.tokens(), p.C);
     const long tiles = ceil_div(p.seq.tokens(), p.L);
-    const long states = (p.dinit || p.seq.cu) ? (long)p.seq.N * (W - 1) : 0;
-    const long total = (tiles + states) * cv, blocks = ceil_div(total, conv::kThreads);
-    if (blocks > kMaxGrid) return COMBA_EUNSUPPORTED;
+    const long total = tiles * cv, blocks = ceil_div(total, conv::kThreads);
+    const long states = (p.dinit || p.seq.cu) ? (long)p.seq.N * (W - 1) * cv : 0, sblocks = ceil_div(states, conv::kThreads);
+    if (blocks > kMaxGrid || sblocks > kMaxGrid) return COMBA_EUNSUPPORTED;
     if (blocks) {
-        if (silu) conv::bwd_kernel<T, W, V, true><<<(unsigned)blocks, conv::kThreads, 0, s>>>(p, tiles, total);
-        else conv::bwd_kernel<T, W, V, false><<<(unsigned)blocks, conv::kThreads, 0, s>>>(p, tiles, total);
+        if (silu) conv::bwd_kernel<T, W, V, true><<<(unsigned)blocks, conv::kThreads, 0, s>>>(p, total);
+        else conv::bwd_kernel<T, W, V, false><<<(unsigned)blocks, conv::kThreads, 0, s>>>(p, total);
+    }
+    if (sblocks) {
+        if (silu) conv::bwd_state_kernel<T, W, V, true><<<(unsigned)sblocks, conv::kThreads, 0, s>>>(p, states);
+        else conv::bwd_state_kernel<T, W, V, false><<<(unsigned)sblocks, conv::kThreads, 0, s>>>(p, states);
     }
     const dim3 grid((unsigned)ceil_div(p.C, 32), W + 1);
     conv::sum_kernel<W><<<grid, 256, 0, s>>>(p.part, dweight, dbias, tiles, p.C);
@@ -89,12 +94,12 @@ int conv_step(const T* x, const float* weight, const float* bias, T* state, T* o
 // f(element type, taps, vector width) for the runtime values.
 #define COMBA_CONV_DISPATCH(f, dtype, W, vec, ...)                                                      \
     ((dtype) == COMBA_BF16                                                                              \
-         ? ((vec) ? ((W) == 4 ? f<bf16, 4, 8>(__VA_ARGS__) : (W) == 3 ? f<bf16, 3, 8>(__VA_ARGS__)      \
-                                                                      : f<bf16, 2, 8>(__VA_ARGS__))     \
+         ? ((vec) ? ((W) == 4 ? f<bf16, 4, 4>(__VA_ARGS__) : (W) == 3 ? f<bf16, 3, 4>(__VA_ARGS__)      \
+                                                                      : f<bf16, 2, 4>(__VA_ARGS__))     \
                   : ((W) == 4 ? f<bf16, 4, 1>(__VA_ARGS__) : (W) == 3 ? f<bf16, 3, 1>(__VA_ARGS__)      \
                                                                       : f<bf16, 2, 1>(__VA_ARGS__)))    \
-         : ((vec) ? ((W) == 4 ? f<float, 4, 8>(__VA_ARGS__) : (W) == 3 ? f<float, 3, 8>(__VA_ARGS__)    \
-                                                                       : f<float, 2, 8>(__VA_ARGS__))   \
+         : ((vec) ? ((W) == 4 ? f<float, 4, 4>(__VA_ARGS__) : (W) == 3 ? f<float, 3, 4>(__VA_ARGS__)    \
+                                                                       : f<float, 2, 4>(__VA_ARGS__))   \
                   : ((W) == 4 ? f<float, 4, 1>(__VA_ARGS__) : (W) == 3 ? f<float, 3, 1>(__VA_ARGS__)    \
                                                                        : f<float, 2, 1>(__VA_ARGS__))))
 
@@ -105,6 +110,7 @@ extern "C" int comba_short_conv_fwd(const void* x, const float* weight, const fl
                                     int silu, int dtype, comba_stream_t stream) {
     if (N < 0 || T < 0 || C < 0 || W < 2 || W > 4 || !dtype_ok(dtype)) return COMBA_EINVAL;
     if (N == 0 || C == 0) return COMBA_OK;
+    if (C > conv::kMaxChannels) return COMBA_EUNSUPPORTED;
     const size_t e = elt_size(dtype), tokens = token_count(cu_seqlens, N, T);
     if (volume(tokens, C) > kMaxElements || volume(N, W - 1, C) > kMaxElements) return COMBA_EINVAL;
     const size_t nx = tokens * C * e, ns = (size_t)N * (W - 1) * C * e;
@@ -119,7 +125,7 @@ extern "C" int comba_short_conv_fwd(const void* x, const float* weight, const fl
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, {x, initial_state, out, final_state});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, out, final_state});
     return COMBA_CONV_DISPATCH(conv_fwd, dtype, W, vec, p, silu != 0, s);
 }
 
@@ -135,6 +141,7 @@ extern "C" int comba_short_conv_bwd(const void* x, const float* weight, const fl
                                     int dtype, void* workspace, size_t workspace_bytes, comba_stream_t stream) {
     if (N < 0 || T < 0 || C < 0 || W < 2 || W > 4 || !dtype_ok(dtype)) return COMBA_EINVAL;
     if (C == 0) return COMBA_OK;
+    if (C > conv::kMaxChannels) return COMBA_EUNSUPPORTED;
     const size_t e = elt_size(dtype), tokens = token_count(cu_seqlens, N, T);
     if (volume(tokens, C) > kMaxElements || volume(N, W - 1, C) > kMaxElements) return COMBA_EINVAL;
     const size_t nx = tokens * C * e, ns = (size_t)N * (W - 1) * C * e;
@@ -155,7 +162,7 @@ extern "C" int comba_short_conv_bwd(const void* x, const float* weight, const fl
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, {x, initial_state, dout, dfinal_state, dx, dinitial_state});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, dout, dfinal_state, dx, dinitial_state});
     return COMBA_CONV_DISPATCH(conv_bwd, dtype, W, vec, p, dweight, dbias, silu != 0, s);
 }
 
@@ -163,6 +170,7 @@ extern "C" int comba_short_conv_step(const void* x, const float* weight, const f
                                      int B, int C, int W, int silu, int dtype, comba_stream_t stream) {
     if (B < 0 || C < 0 || W < 2 || W > 4 || !dtype_ok(dtype)) return COMBA_EINVAL;
     if (B == 0 || C == 0) return COMBA_OK;
+    if (C > conv::kMaxChannels) return COMBA_EUNSUPPORTED;
     const size_t e = elt_size(dtype);
     if (volume(B, W, C) > kMaxElements) return COMBA_EINVAL;
     const size_t nx = (size_t)B * C * e;
@@ -170,23 +178,23 @@ extern "C" int comba_short_conv_step(const void* x, const float* weight, const f
     const Arg outs[] = {{state, nx * (W - 1), e, false}, {out, nx, e, false}};
     if (!args_ok(ins, outs)) return COMBA_EINVAL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, {x, state, out});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, state, out});
     const bool act = silu != 0;
     if (dtype == COMBA_BF16) {
         const auto* xt = static_cast<const bf16*>(x);
         auto *st = static_cast<bf16*>(state), *ot = static_cast<bf16*>(out);
-        if (vec) return W == 4 ? conv_step<bf16, 4, 8>(xt, weight, bias, st, ot, B, C, act, s)
-                      : W == 3 ? conv_step<bf16, 3, 8>(xt, weight, bias, st, ot, B, C, act, s)
-                               : conv_step<bf16, 2, 8>(xt, weight, bias, st, ot, B, C, act, s);
+        if (vec) return W == 4 ? conv_step<bf16, 4, 4>(xt, weight, bias, st, ot, B, C, act, s)
+                      : W == 3 ? conv_step<bf16, 3, 4>(xt, weight, bias, st, ot, B, C, act, s)
+                               : conv_step<bf16, 2, 4>(xt, weight, bias, st, ot, B, C, act, s);
         return W == 4 ? conv_step<bf16, 4, 1>(xt, weight, bias, st, ot, B, C, act, s)
              : W == 3 ? conv_step<bf16, 3, 1>(xt, weight, bias, st, ot, B, C, act, s)
                       : conv_step<bf16, 2, 1>(xt, weight, bias, st, ot, B, C, act, s);
     }
     const auto* xt = static_cast<const float*>(x);
     auto *st = static_cast<float*>(state), *ot = static_cast<float*>(out);
-    if (vec) return W == 4 ? conv_step<float, 4, 8>(xt, weight, bias, st, ot, B, C, act, s)
-                  : W == 3 ? conv_step<float, 3, 8>(xt, weight, bias, st, ot, B, C, act, s)
-                           : conv_step<float, 2, 8>(xt, weight, bias, st, ot, B, C, act, s);
+    if (vec) return W == 4 ? conv_step<float, 4, 4>(xt, weight, bias, st, ot, B, C, act, s)
+                  : W == 3 ? conv_step<float, 3, 4>(xt, weight, bias, st, ot, B, C, act, s)
+                           : conv_step<float, 2, 4>(xt, weight, bias, st, ot, B, C, act, s);
     return W == 4 ? conv_step<float, 4, 1>(xt, weight, bias, st, ot, B, C, act, s)
          : W == 3 ? conv_step<float, 3, 1>(xt, weight, bias, st, ot, B, C, act, s)
                   : conv_step<float, 2, 1>(xt, weight, bias, st, ot, B, C, act, s);
@@ -529,7 +537,7 @@ extern "C" int comba_gated_norm_fwd(const void* x, const void* gate, const float
     p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, gate, weight, out});
+    const bool vec = vector_rows(D, kVec, 16, {x, gate, weight, out});
     if (dtype == COMBA_BF16) return vec ? gated_fwd<bf16, true>(p, s) : gated_fwd<bf16, false>(p, s);
     return vec ? gated_fwd<float, true>(p, s) : gated_fwd<float, false>(p, s);
 }
@@ -557,7 +565,7 @@ extern "C" int comba_gated_norm_bwd(const void* x, const void* gate, const float
     p.tpr = norm::row_threads(D);
     const long blocks = rows > 0 ? norm::bwd_blocks(rows, D, norm::kGatedBlocks) : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, gate, weight, dout, dx, dgate});
+    const bool vec = vector_rows(D, kVec, 16, {x, gate, weight, dout, dx, dgate});
     if (blocks) {
         const int st = dtype == COMBA_BF16 ? (vec ? gated_bwd<bf16, true>(p, (unsigned)blocks, s) : gated_bwd<bf16, false>(p, (unsigned)blocks, s))
                                            : (vec ? gated_bwd<float, true>(p, (unsigned)blocks, s) : gated_bwd<float, false>(p, (unsigned)blocks, s));
@@ -582,7 +590,7 @@ extern "C" int comba_residual_norm_fwd(const void* x, const void* residual, cons
     p.x = x; p.residual = residual; p.weight = weight; p.scale = scale; p.post = post_weight; p.out = out; p.h = h;
     p.rows = rows; p.D = D; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.tpr = norm::row_threads(D);
-    const bool vec = vector_rows(D, {x, residual, weight, scale, post_weight, out, h});
+    const bool vec = vector_rows(D, kVec, 16, {x, residual, weight, scale, post_weight, out, h});
     return COMBA_RESIDUAL_DISPATCH(residual_fwd, dtype, residual_dtype, vec, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -616,7 +624,7 @@ extern "C" int comba_residual_norm_bwd(const void* x, const void* h, const float
     p.tpr = norm::row_threads(D);
     const long blocks = rows > 0 ? norm::bwd_blocks(rows, D, norm::kResidualBlocks) : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(D, {x, h, weight, scale, post_weight, dy, dh, dx, dresidual});
+    const bool vec = vector_rows(D, kVec, 16, {x, h, weight, scale, post_weight, dy, dh, dx, dresidual});
     if (blocks)
         if (int st = COMBA_RESIDUAL_DISPATCH(residual_bwd, dtype, residual_dtype, vec, p, (unsigned)blocks, s)) return st;
     sum_rows_kernel<<<dim3((unsigned)ceil_div(D, 32), 3), 256, 0, s>>>(

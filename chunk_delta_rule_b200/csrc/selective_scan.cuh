@@ -19,7 +19,6 @@ using namespace blk;
 constexpr int kThreads = 128;
 constexpr int kBatch = 4;        // tokens whose operands a lane holds at a time
 constexpr int kSub = 8;          // tokens between two stored states of the backward
-constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Params {
     const void *x, *dt, *Bm, *Cm, *z, *dout;
@@ -40,32 +39,6 @@ struct Params {
     int* status;
 };
 
-// 2^v for v <= 0 by the hardware's approximation (relative error 2^-22).
-__device__ __forceinline__ float exp2_fast(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Pairs of fp32 values in a 64-bit register: one instruction for two products or sums, so
-// that the issue slots do not bound the state's update.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float a, float b) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(Pair v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ Pair exp2_pair(Pair v) {
     float a, b;
     unpair(v, a, b);
@@ -150,8 +123,6 @@ __device__ __forceinline__ void store_group(void* base, long o, const float (&f)
             if (i < count) p[i] = r.v[i];
     }
 }
-
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Four elements of B or C, as they are stored.
 template <typename T> struct Raw4;

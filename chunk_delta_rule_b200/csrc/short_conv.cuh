@@ -5,9 +5,11 @@
 //
 // with the W-1 inputs before a sequence's first token taken from its carried state.  Every
 // token is read and written once, so the kernels are bound by HBM bandwidth: a thread
-// keeps the filter and the last W-1 inputs of 8 neighbouring channels in registers and
+// keeps the filter and the last W-1 inputs of 4 neighbouring channels in registers and
 // walks a tile of tokens.
 #pragma once
+
+#include <limits.h>
 
 #include "block_common.cuh"
 
@@ -17,6 +19,8 @@ namespace conv {
 using namespace blk;
 
 constexpr int kThreads = 128;
+constexpr int kMaxChannels = 1 << 23;   // a tile of up to 128 tokens then fits 32-bit offsets
+constexpr int kChannels = 4;      // that a thread handles on the vector path
 
 struct Params {
     const float *weight, *bias;     // [C, W], [C] or null
@@ -55,6 +59,47 @@ __device__ __forceinline__ void load_x(const Params& p, int n, long s, long t, i
     }
 }
 
+// A thread's V channels of the next tokens, on their way into a ring of its own in shared
+// memory: rows in flight do not cost registers, which alone held too few to cover HBM's
+// latency (forward of B8 T4096 C6144 bf16: 209 us with 4 rows a thread in registers).
+// Rows go in and out kAhead at a time; K arrays are read side by side.
+constexpr int kAhead = 4;
+template <typename T, int V, int K>
+struct Ring {
+    static constexpr int GROUPS = V * sizeof(T) > 8 ? 2 : 4, ROWS = GROUPS * kAhead;
+    struct alignas(V * sizeof(T)) Row {
+        T v[V];
+    };
+    using Storage = Row[ROWS][K][kThreads];
+    Storage& mem;
+    __device__ __forceinline__ void put(int slot, int k, const T* p) {
+        Row* r = &mem[slot][k][threadIdx.x];
+        if constexpr (sizeof(Row) >= 4) {
+            const unsigned at = (unsigned)__cvta_generic_to_shared(r);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(p), "n"((int)sizeof(Row)) : "memory");
+        } else {
+            *r = *reinterpret_cast<const Row*>(p);
+        }
+    }
+    __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    template <int LEFT>
+    __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+    __device__ __forceinline__ void get(int slot, int k, float (&x)[V]) const { load_v<V>(mem[slot][k][threadIdx.x].v, x); }
+};
+
+// acc[i] += a[i] * b[i], two at a time.
+template <int V>
+__device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], float (&acc)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            unpair(fma2(pair(a[i], a[i + 1]), pair(b[i], b[i + 1]), pair(acc[i], acc[i + 1])), acc[i], acc[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(a[i], b[i], acc[i]);
+    }
+}
+
 // One thread per (tile of tokens, V channels), then one per (sequence, state row, V
 // channels) for the final states and the check of the bounds.
 template <typename T, int W, int V, bool SILU>
@@ -80,6 +125,9 @@ fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
         }
         return;
     }
+    using R = Ring<T, V, 1>;
+    __shared__ typename R::Storage mem;
+    R ring{mem};
     const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
     float w[W][V], b[V];
     load_filter<W, V>(p, c, w, b);
@@ -95,24 +143,91 @@ fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
         for (int j = 0; j < W - 1; ++j) load_x<T, W, V>(p, n, s, t - (W - 1) + j, c, h[j]);
         const T* xp = static_cast<const T*>(p.x) + t * p.C + c;
         T* op = static_cast<T*>(p.out) + t * p.C + c;
-#pragma unroll 4
-        for (; t < stop; ++t, xp += p.C, op += p.C) {
-            load_v<V>(xp, h[W - 1]);
-            float y[V];
+        // the ring runs GROUPS - 1 groups ahead (past the end: the last token's, not used);
+        // offsets within a tile fit 32 bits
+        const int last = (int)(stop - 1 - t);
+        const unsigned C = p.C;
+        auto fetch = [&](int at) {
+            if (at <= last)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                y[i] = b[i];
+                for (int k = 0; k < kAhead; ++k) ring.put((at + k) % R::ROWS, 0, xp + min(at + k, last) * C);
+            ring.commit();
+        };
 #pragma unroll
-                for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], h[j][i], y[i]);
-                if (SILU) y[i] = silu(y[i]);
+        for (int k = 0; k < R::GROUPS - 1; ++k) fetch(k * kAhead);
+        for (int k0 = 0; k0 <= last; k0 += kAhead) {
+            fetch(k0 + R::ROWS - kAhead);
+            ring.template wait<R::GROUPS - 1>();
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (k0 + k > last) break;
+                ring.get((k0 + k) % R::ROWS, 0, h[W - 1]);
+                float y[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] = b[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) fma_v<V>(w[j], h[j], y);
+                if (SILU)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
+                store_v<V>(op + (k0 + k) * C, y);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
             }
-            store_v<V>(op, y);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
         }
+        ring.template wait<0>();
+        t = stop;
     }
+}
+
+// d pre of one token from its cotangent d; its input is h[W-1], the W-1 before it h[0 .. W-2].
+template <int W, int V, bool SILU>
+__device__ __forceinline__ void dpre_of(const float (&w)[W][V], const float (&b)[V], const float (&h)[W][V], float (&d)[V]) {
+    if (SILU) {
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = b[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) fma_v<V>(w[j], h[j], y);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= dsilu(y[i]);
+    }
+}
+
+// Cotangent of the initial state's row m, the input W-1-m before the first token, and the
+// check of the bounds: one thread per (sequence, row, V channels).
+template <typename T, int W, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads)
+bwd_state_kernel(const __grid_constant__ Params p, long total) {
+    const long id = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int cv = p.C / V, c = (int)(id % cv) * V;
+    const int n = (int)(id / cv / (W - 1)), m = (int)(id / cv % (W - 1));
+    long s, e;
+    if (!p.seq.bounds(n, s, e)) {
+        atomicCAS(p.status, 0, COMBA_EINVAL);
+        return;
+    }
+    if (!p.dinit) return;
+    float w[W][V], b[V], g[V];
+    load_filter<W, V>(p, c, w, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = 0.f;
+    const long at = m - (e - s);   // its row of the final state, of a sequence shorter than that
+    if (p.dfin && at >= 0) load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + at) * p.C + c, g);
+#pragma unroll 1
+    for (int k = 0; k <= m && s + k < e; ++k) {   // token s + k reads it through tap m - k
+        float h[W][V], d[V];
+#pragma unroll
+        for (int j = 0; j < W; ++j) load_x<T, W, V>(p, n, s, s + k - (W - 1) + j, c, h[j]);
+        load_v<V>(static_cast<const T*>(p.dout) + (s + k) * p.C + c, d);
+        dpre_of<W, V, SILU>(w, b, h, d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = fmaf(p.weight[(long)(c + i) * W + m - k], d[i], g[i]);
+    }
+    store_v<V>(static_cast<T*>(p.dinit) + ((long)n * (W - 1) + m) * p.C + c, g);
 }
 
 // Backward of one tile.  With dpre_t = dout_t silu'(pre_t) (pre recomputed),
@@ -120,61 +235,21 @@ fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
 //   dw_j = sum_t dpre_t x_{t-W+1+j},   dbias = sum_t dpre_t.
 // A thread walks its tokens and W-1 more of the same sequence, whose dpre it forms again
 // for the tile's last dx; the sums take the tile's own tokens only and go to `part`.
-// dpre of one token: its input is h[W-1], the W-1 before it h[0 .. W-2].
 template <typename T, int W, int V, bool SILU>
-__device__ __forceinline__ void dpre_of(const Params& p, long t, int c, const float (&w)[W][V], const float (&b)[V],
-                                        const float (&h)[W][V], float (&d)[V]) {
-    load_v<V>(static_cast<const T*>(p.dout) + t * p.C + c, d);
-    if (SILU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float y = b[i];
-#pragma unroll
-            for (int j = 0; j < W; ++j) y = fmaf(w[j][i], h[j][i], y);
-            d[i] *= dsilu(y);
-        }
-    }
-}
-
-template <typename T, int W, int V, bool SILU>
-__global__ void __launch_bounds__(kThreads)
-bwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
+__global__ void __launch_bounds__(kThreads, 4)
+bwd_kernel(const __grid_constant__ Params p, long total) {
     const long id = (long)blockIdx.x * kThreads + threadIdx.x;
     if (id >= total) return;
     const int cv = p.C / V;
     const long row = id / cv;
     const int c = (int)(id - row * cv) * V;
+    const T* xb = static_cast<const T*>(p.x) + c;
+    const T* ob = static_cast<const T*>(p.dout) + c;
+    using R = Ring<T, V, 2>;
+    __shared__ typename R::Storage mem;
+    R ring{mem};
     float w[W][V], b[V];
     load_filter<W, V>(p, c, w, b);
-    if (row >= tiles) {
-        // cotangent of the initial state's row m, the input W-1-m before the first token
-        const long q = row - tiles;
-        const int n = (int)(q / (W - 1)), m = (int)(q % (W - 1));
-        long s, e;
-        if (!p.seq.bounds(n, s, e)) {
-            atomicCAS(p.status, 0, COMBA_EINVAL);
-            return;
-        }
-        if (!p.dinit) return;
-        float g[V];
-        const long at = m - (e - s);   // its row of the final state, of a sequence shorter than that
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = 0.f;
-        if (p.dfin && at >= 0) load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + at) * p.C + c, g);
-        for (int k = 0; k <= m && s + k < e; ++k) {   // token s + k reads it through tap m - k
-            float h[W][V], d[V];
-#pragma unroll
-            for (int j = 0; j < W; ++j) load_x<T, W, V>(p, n, s, s + k - (W - 1) + j, c, h[j]);
-            dpre_of<T, W, V, SILU>(p, s + k, c, w, b, h, d);
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (j == m - k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[i] = fmaf(w[j][i], d[i], g[i]);
-        }
-        store_v<V>(static_cast<T*>(p.dinit) + ((long)n * (W - 1) + m) * p.C + c, g);
-        return;
-    }
     const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
     float dw[W][V], db[V];
 #pragma unroll
@@ -198,39 +273,25 @@ bwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
 #pragma unroll
             for (int i = 0; i < V; ++i) g[j][i] = 0.f;
         }
-#pragma unroll 2
-        for (; t < stop + W - 1; ++t) {
-            float d[V];
-            if (t < e) {
-                load_v<V>(static_cast<const T*>(p.x) + t * p.C + c, h[W - 1]);
-                dpre_of<T, W, V, SILU>(p, t, c, w, b, h, d);
-            } else {
+        // tokens are counted from `from` on; offsets within a tile fit 32 bits
+        const int count = (int)(stop - from), rest = (int)min(e - from, (long)INT_MAX);
+        const unsigned C = p.C;
+        const T *xp = xb + from * p.C, *dp = ob + from * p.C;
+        T* gp = static_cast<T*>(p.dx) + from * p.C + c;
+        // adds a token's d to the open dx and closes that of the token W - 1 before it
+        auto close = [&](int at, const float (&d)[V]) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[i] = h[W - 1][i] = 0.f;
-            }
+            for (int i = 0; i < V; ++i) g[W - 1][i] = w[W - 1][i] * d[i];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g[W - 1][i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < W; ++j) g[j][i] = fmaf(w[j][i], d[i], g[j][i]);
-            }
-            if (t < stop) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    db[i] += d[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d[i], h[j][i], dw[j][i]);
-                }
-            }
-            const long o = t - (W - 1);   // the token whose dx is complete
-            if (o >= from) {
-                if (p.dfin && o >= e - (W - 1)) {
+            for (int j = 0; j < W - 1; ++j) fma_v<V>(w[j], d, g[j]);
+            if (at >= W - 1) {
+                if (p.dfin && at >= rest) {
                     float f[V];
-                    load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + (o - (e - (W - 1)))) * p.C + c, f);
+                    load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + (at - rest)) * p.C + c, f);
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[0][i] += f[i];
                 }
-                store_v<V>(static_cast<T*>(p.dx) + o * p.C + c, g[0]);
+                store_v<V>(gp + (at - (W - 1)) * C, g[0]);
             }
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
@@ -239,6 +300,49 @@ bwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
                     h[j][i] = h[j + 1][i];
                     g[j][i] = g[j + 1][i];
                 }
+        };
+        auto fetch = [&](int at) {   // past the tile: its last token's, not used
+            if (at < count)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const unsigned o = min(at + k, count - 1) * C;
+                    ring.put((at + k) % R::ROWS, 0, xp + o);
+                    ring.put((at + k) % R::ROWS, 1, dp + o);
+                }
+            ring.commit();
+        };
+#pragma unroll
+        for (int k = 0; k < R::GROUPS - 1; ++k) fetch(k * kAhead);
+        for (int k0 = 0; k0 < count; k0 += kAhead) {
+            fetch(k0 + R::ROWS - kAhead);
+            ring.template wait<R::GROUPS - 1>();
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (k0 + k >= count) break;
+                float d[V];
+                ring.get((k0 + k) % R::ROWS, 0, h[W - 1]);
+                ring.get((k0 + k) % R::ROWS, 1, d);
+                dpre_of<W, V, SILU>(w, b, h, d);
+#pragma unroll
+                for (int i = 0; i < V; ++i) db[i] += d[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) fma_v<V>(d, h[j], dw[j]);
+                close(k0 + k, d);
+            }
+        }
+        ring.template wait<0>();
+        // the W-1 tokens behind the tile; past the sequence's end there is nothing to add
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float d[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[i] = h[W - 1][i] = 0.f;
+            if (count + k < rest) {
+                load_v<V>(xp + (count + k) * C, h[W - 1]);
+                load_v<V>(dp + (count + k) * C, d);
+                dpre_of<W, V, SILU>(w, b, h, d);
+            }
+            close(count + k, d);
         }
         t = stop;
     }
@@ -304,7 +408,7 @@ step_kernel(const T* __restrict__ x, const float* __restrict__ weight, const flo
 // write fewer partial sums; short ones give enough threads when the tokens are few.
 inline int tile_tokens(long tokens, int cv, int most) {
     int L = most;
-    while (L > 4 && ceil_div(tokens, L) * cv < (long)kSMs * 512) L /= 2;
+    while (L > 4 && ceil_div(tokens, L) * cv < (long)kSMs * 1024) L /= 2;
     return L;
 }
 

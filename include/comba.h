@@ -402,8 +402,8 @@ int comba_state_compose(const float* RM, const float* S0, float* S_start, int B,
  * (pre_t itself when silu == 0).  The W - 1 inputs before a sequence's first token are
  * its initial_state [nseq, W-1, C], oldest first (NULL: zeros); final_state [nseq, W-1, C]
  * (NULL: not written) receives the last W - 1 inputs, which continue the sequence in
- * another call or in comba_short_conv_step.  W in {2, 3, 4}; weight [C, W], bias [C] or
- * NULL.  final_state must not overlap initial_state.
+ * another call or in comba_short_conv_step.  W in {2, 3, 4}; C <= 2^23
+ * (COMBA_EUNSUPPORTED above); weight [C, W], bias [C] or NULL.  final_state must not overlap initial_state.
  */
 int comba_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
                          void* out, void* final_state, const int* cu_seqlens, int nseq, int T, int C, int W,
