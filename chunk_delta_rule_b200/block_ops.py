@@ -20,14 +20,20 @@ __all__ = ["short_conv", "short_conv_bwd", "short_conv_step", "selective_scan", 
            "selective_scan_step", "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_F32 = torch.float32
 
 
-def _tensor(t, name: str, dtype, shape, device, optional: bool = False) -> None:
+def _tensor(t, name: str, dtype, shape, index: int, optional: bool = False) -> None:
+    """Refuses ``t`` unless it is a contiguous tensor of this type and shape on CUDA device
+    ``index`` (decode steps are short enough for the checks to count: one expression
+    passes what is right, and only a wrong tensor is looked at closely)."""
     if t is None and optional:
         return
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.is_cuda and t.get_device() == index):
+        return
     _cdr._check(t, name, dtype, shape)
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
 
 
 def _element(t, name: str) -> torch.dtype:
@@ -38,32 +44,44 @@ def _element(t, name: str) -> torch.dtype:
     return t.dtype
 
 
-class _Call:
-    """One call of the library: its buffers, of which those allocated here are kept for
-    the caller's stream, and the device and stream it runs on."""
+def _device(t, name: str) -> int:
+    """The CUDA device of a call, from its first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    return t.get_device()
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.made = device, stream, []
+
+class _Call:
+    """One call of the library: its device and stream, and the buffers that are allocated
+    here, which are kept for the caller's stream."""
+    __slots__ = ("index", "stream", "made")
+
+    def __init__(self, index: int, stream):
+        self.index, self.stream, self.made = index, stream, []
 
     def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+        t = torch.empty(shape, dtype=dtype, device=self.index)
         self.made.append(t)
         return t
 
     def workspace(self, nbytes: int, given: Optional[torch.Tensor]):
         if given is None:
             return self.new((max(int(nbytes), 16),), torch.uint8)
-        if given.dtype != torch.uint8 or given.device != self.device or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        if given.dtype != torch.uint8 or not given.is_cuda or given.get_device() != self.index or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{self.index}")
         return given
 
     def __call__(self, name: str, *args) -> None:
-        lib = _cdr.library()
-        args = [_cdr._ptr(a) if a is None or isinstance(a, torch.Tensor) else a for a in args]
-        with torch.cuda.device(self.device):
-            st = getattr(lib, name)(*args, _cdr._stream_handle(self.device, self.stream))
-            for t in self.made:
-                _cdr._keep_for_stream(t, self.device, self.stream)
+        fn = getattr(_cdr.library(), name)
+        args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+        if torch.cuda.current_device() == self.index and self.stream is None:
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(self.index))
+        else:
+            device = torch.device("cuda", self.index)
+            with torch.cuda.device(device):
+                st = fn(*args, _cdr._stream_handle(device, self.stream))
+                for t in self.made:
+                    _cdr._keep_for_stream(t, device, self.stream)
         if st != 0:
             raise _cdr.CombaError(st, name)
 
@@ -86,7 +104,7 @@ def _filter(weight, C: int, dev):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [C, W]")
     W = weight.shape[1]
-    _tensor(weight, "weight", torch.float32, (C, W), dev)
+    _tensor(weight, "weight", _F32, (C, W), dev)
     return W
 
 
@@ -99,16 +117,16 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     [C,W], bias [C] or None fp32; initial_state [N,W-1,C] (the inputs before each
     sequence, oldest first) or None.  Returns (out like x, final_state [N,W-1,C] or None)."""
     lead, N, T, C = _tokens(x, cu_seqlens)
-    dt, dev = x.dtype, x.device
-    _tensor(x, "x", dt, (*lead, C), None)
+    dt, dev, shape = x.dtype, _device(x, "x"), x.shape
+    _tensor(x, "x", dt, shape, dev)
     W = _filter(weight, C, dev)
-    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    _tensor(bias, "bias", _F32, (C,), dev, True)
     _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
     call = _Call(dev, stream)
     if out is None:
-        out = call.new((*lead, C), dt)
-    _tensor(out, "out", dt, (*lead, C), dev)
+        out = call.new(shape, dt)
+    _tensor(out, "out", dt, shape, dev)
     if final_state is None and return_state:
         final_state = call.new((N, W - 1, C), dt)
     _tensor(final_state, "final_state", dt, (N, W - 1, C), dev, True)
@@ -126,17 +144,17 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bi
     and dinitial_state (None without initial_state).  ``workspace``: a uint8 device tensor
     of at least comba_short_conv_bwd_workspace_size bytes, for this call alone."""
     lead, N, T, C = _tokens(x, cu_seqlens)
-    dt, dev = x.dtype, x.device
-    _tensor(x, "x", dt, (*lead, C), None)
+    dt, dev, shape = x.dtype, _device(x, "x"), x.shape
+    _tensor(x, "x", dt, shape, dev)
     W = _filter(weight, C, dev)
-    _tensor(dout, "dout", dt, (*lead, C), dev)
-    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    _tensor(dout, "dout", dt, shape, dev)
+    _tensor(bias, "bias", _F32, (C,), dev, True)
     _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
     _tensor(dfinal_state, "dfinal_state", dt, (N, W - 1, C), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
     call = _Call(dev, stream)
-    g = {"dx": call.new((*lead, C), dt), "dweight": call.new((C, W), torch.float32),
-         "dbias": None if bias is None else call.new((C,), torch.float32),
+    g = {"dx": call.new(shape, dt), "dweight": call.new((C, W), _F32),
+         "dbias": None if bias is None else call.new((C,), _F32),
          "dinitial_state": None if initial_state is None else call.new((N, W - 1, C), dt)}
     need = _cdr.library().comba_short_conv_bwd_workspace_size(N, T, C, W, int(cu_seqlens is not None))
     ws = call.workspace(need, workspace)
@@ -153,11 +171,11 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
-    dev = x.device
-    _tensor(x, "x", dt, (B, C), None)
+    dev = _device(x, "x")
+    _tensor(x, "x", dt, (B, C), dev)
     W = _filter(weight, C, dev)
     _tensor(state, "state", dt, (B, W - 1, C), dev)
-    _tensor(bias, "bias", torch.float32, (C,), dev, True)
+    _tensor(bias, "bias", _F32, (C,), dev, True)
     call = _Call(dev, stream)
     if out is None:
         out = call.new((B, C), dt)
@@ -168,18 +186,18 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
 
 def _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z):
     """(groups, states) of a scan whose token tensors have the leading shape ``lead``."""
-    et, dev = x.dtype, x.device
-    _tensor(x, "x", et, (*lead, C), None)
-    _tensor(dt, "dt", et, (*lead, C), dev)
+    et, dev, shape = x.dtype, _device(x, "x"), x.shape
+    _tensor(x, "x", et, shape, dev)
+    _tensor(dt, "dt", et, shape, dev)
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
         raise ValueError("Bm must be [..., G, N]")
     G, N = Bm.shape[-2:]
-    _tensor(A_log, "A_log", torch.float32, (C, N), dev)
+    _tensor(A_log, "A_log", _F32, (C, N), dev)
     _tensor(Bm, "Bm", et, (*lead, G, N), dev)
     _tensor(Cm, "Cm", et, (*lead, G, N), dev)
-    _tensor(D, "D", torch.float32, (C,), dev, True)
-    _tensor(dt_bias, "dt_bias", torch.float32, (C,), dev, True)
-    _tensor(z, "z", et, (*lead, C), dev, True)
+    _tensor(D, "D", _F32, (C,), dev, True)
+    _tensor(dt_bias, "dt_bias", _F32, (C,), dev, True)
+    _tensor(z, "z", et, shape, dev, True)
     return G, N
 
 
@@ -199,16 +217,16 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: t
     sequences run in pieces), for this call alone."""
     lead, nseq, T, C = _tokens(x, cu_seqlens)
     G, N = _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
-    et, dev = x.dtype, x.device
-    _tensor(h0, "h0", torch.float32, (nseq, C, N), dev, True)
+    et, dev, shape = x.dtype, _device(x, "x"), x.shape
+    _tensor(h0, "h0", _F32, (nseq, C, N), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
     call = _Call(dev, stream)
     if out is None:
-        out = call.new((*lead, C), et)
-    _tensor(out, "out", et, (*lead, C), dev)
+        out = call.new(shape, et)
+    _tensor(out, "out", et, shape, dev)
     if h_final is None and return_state:
-        h_final = call.new((nseq, C, N), torch.float32)
-    _tensor(h_final, "h_final", torch.float32, (nseq, C, N), dev, True)
+        h_final = call.new((nseq, C, N), _F32)
+    _tensor(h_final, "h_final", _F32, (nseq, C, N), dev, True)
     need = _cdr.library().comba_selective_scan_fwd_workspace_size(nseq, T, C, G, N, int(cu_seqlens is not None))
     ws = call.workspace(need, workspace) if need or workspace is not None else None
     call("comba_selective_scan_fwd", x, dt, A_log, Bm, Cm, D, dt_bias, z, h0, out, h_final, cu_seqlens, nseq, T, C, G, N,
@@ -228,17 +246,17 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B
     comba_selective_scan_bwd_workspace_size bytes, for this call alone."""
     lead, nseq, T, C = _tokens(x, cu_seqlens)
     G, N = _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
-    et, dev, f32 = x.dtype, x.device, torch.float32
-    _tensor(dout, "dout", et, (*lead, C), dev)
+    et, dev, f32, shape = x.dtype, _device(x, "x"), _F32, x.shape
+    _tensor(dout, "dout", et, shape, dev)
     _tensor(h0, "h0", f32, (nseq, C, N), dev, True)
     _tensor(dh_final, "dh_final", f32, (nseq, C, N), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
     call = _Call(dev, stream)
-    g = {"dx": call.new((*lead, C), et), "ddt": call.new((*lead, C), et), "dA_log": call.new((C, N), f32),
+    g = {"dx": call.new(shape, et), "ddt": call.new(shape, et), "dA_log": call.new((C, N), f32),
          "dBm": call.new((*lead, G, N), et), "dCm": call.new((*lead, G, N), et),
          "dD": None if D is None else call.new((C,), f32),
          "ddt_bias": None if dt_bias is None else call.new((C,), f32),
-         "dz": None if z is None else call.new((*lead, C), et),
+         "dz": None if z is None else call.new(shape, et),
          "dh0": None if h0 is None else call.new((nseq, C, N), f32)}
     need = _cdr.library().comba_selective_scan_bwd_workspace_size(nseq, T, C, G, N, int(cu_seqlens is not None))
     ws = call.workspace(need, workspace)
@@ -258,9 +276,9 @@ def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
-    dev = x.device
+    dev = _device(x, "x")
     G, N = _scan_inputs((B,), C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
-    _tensor(h, "h", torch.float32, (B, C, N), dev)
+    _tensor(h, "h", _F32, (B, C, N), dev)
     call = _Call(dev, stream)
     if out is None:
         out = call.new((B, C), et)
@@ -283,10 +301,10 @@ def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: f
     dimension, e.g. chunk_fwd's out [B,T,H,dv] per head.  x, gate [..., D] bf16 or fp32;
     weight [D] fp32; D <= 8192.  Returns out like x."""
     dt, D, rows = _norm_rows(x)
-    dev = x.device
-    _tensor(x, "x", dt, x.shape, None)
+    dev = _device(x, "x")
+    _tensor(x, "x", dt, x.shape, dev)
     _tensor(gate, "gate", dt, x.shape, dev)
-    _tensor(weight, "weight", torch.float32, (D,), dev)
+    _tensor(weight, "weight", _F32, (D,), dev)
     call = _Call(dev, stream)
     if out is None:
         out = call.new(tuple(x.shape), dt)
@@ -300,13 +318,13 @@ def gated_norm_bwd(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, do
     """comba_gated_norm_bwd: gradients of <dout, out> of gated_norm, as a dict of dx, dgate
     (like x) and dweight [D] fp32."""
     dt, D, rows = _norm_rows(x)
-    dev = x.device
-    _tensor(x, "x", dt, x.shape, None)
+    dev = _device(x, "x")
+    _tensor(x, "x", dt, x.shape, dev)
     _tensor(gate, "gate", dt, x.shape, dev)
-    _tensor(weight, "weight", torch.float32, (D,), dev)
+    _tensor(weight, "weight", _F32, (D,), dev)
     _tensor(dout, "dout", dt, x.shape, dev)
     call = _Call(dev, stream)
-    g = {"dx": call.new(tuple(x.shape), dt), "dgate": call.new(tuple(x.shape), dt), "dweight": call.new((D,), torch.float32)}
+    g = {"dx": call.new(tuple(x.shape), dt), "dgate": call.new(tuple(x.shape), dt), "dweight": call.new((D,), _F32)}
     ws = call.workspace(_cdr.library().comba_gated_norm_bwd_workspace_size(rows, D), workspace)
     call("comba_gated_norm_bwd", x, gate, weight, dout, g["dx"], g["dgate"], g["dweight"], rows, D, float(eps), _DTYPE[dt],
          ws, ws.numel())
@@ -315,15 +333,15 @@ def gated_norm_bwd(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, do
 
 def _residual_inputs(x, stream_t, name, weight, scale, post_weight):
     dt, D, rows = _norm_rows(x)
-    dev = x.device
-    _tensor(x, "x", dt, x.shape, None)
+    dev = _device(x, "x")
+    _tensor(x, "x", dt, x.shape, dev)
     rt = _element(stream_t, name)
-    if rt not in (dt, torch.float32):
+    if rt not in (dt, _F32):
         raise TypeError(f"{name} must be fp32 or of x's dtype (got {rt})")
     _tensor(stream_t, name, rt, x.shape, dev)
-    _tensor(weight, "weight", torch.float32, (D,), dev)
-    _tensor(scale, "scale", torch.float32, (D,), dev, True)
-    _tensor(post_weight, "post_weight", torch.float32, (D,), dev, True)
+    _tensor(weight, "weight", _F32, (D,), dev)
+    _tensor(scale, "scale", _F32, (D,), dev, True)
+    _tensor(post_weight, "post_weight", _F32, (D,), dev, True)
     return dt, rt, D, rows, dev
 
 
@@ -358,7 +376,7 @@ def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dy
     _tensor(dy, "dy", dt, x.shape, dev)
     _tensor(dh, "dh", rt, x.shape, dev, True)
     call = _Call(dev, stream)
-    f32 = torch.float32
+    f32 = _F32
     g = {"dx": call.new(tuple(x.shape), dt), "dresidual": call.new(tuple(x.shape), rt), "dweight": call.new((D,), f32),
          "dscale": None if scale is None else call.new((D,), f32),
          "dpost_weight": None if post_weight is None else call.new((D,), f32)}
