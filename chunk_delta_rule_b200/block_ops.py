@@ -52,15 +52,20 @@ def _device(t, name: str) -> int:
 
 
 class _Call:
-    """One call of the library: its device and stream, and the buffers that are allocated
-    here, which are kept for the caller's stream."""
-    __slots__ = ("index", "stream", "made")
+    """One call of the library: the device (of its first tensor), the stream, and the
+    buffers that are allocated here, which are kept for the caller's stream."""
+    __slots__ = ("first", "index", "stream", "made")
 
-    def __init__(self, index: int, stream):
-        self.index, self.stream, self.made = index, stream, []
+    def __init__(self, first, index: int, stream):
+        self.first, self.index, self.stream, self.made = first, index, stream, []
 
     def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.index)
+        t = self.first.new_empty(shape, dtype=dtype)
+        self.made.append(t)
+        return t
+
+    def like(self, t):
+        t = torch.empty_like(t)   # of a contiguous tensor: the quickest allocation
         self.made.append(t)
         return t
 
@@ -123,10 +128,11 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     _tensor(bias, "bias", _F32, (C,), dev, True)
     _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
-        out = call.new(shape, dt)
-    _tensor(out, "out", dt, shape, dev)
+        out = call.like(x)
+    else:
+        _tensor(out, "out", dt, shape, dev)
     if final_state is None and return_state:
         final_state = call.new((N, W - 1, C), dt)
     _tensor(final_state, "final_state", dt, (N, W - 1, C), dev, True)
@@ -152,8 +158,8 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bi
     _tensor(initial_state, "initial_state", dt, (N, W - 1, C), dev, True)
     _tensor(dfinal_state, "dfinal_state", dt, (N, W - 1, C), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev, True)
-    call = _Call(dev, stream)
-    g = {"dx": call.new(shape, dt), "dweight": call.new((C, W), _F32),
+    call = _Call(x, dev, stream)
+    g = {"dx": call.like(x), "dweight": call.new((C, W), _F32),
          "dbias": None if bias is None else call.new((C,), _F32),
          "dinitial_state": None if initial_state is None else call.new((N, W - 1, C), dt)}
     need = _cdr.library().comba_short_conv_bwd_workspace_size(N, T, C, W, int(cu_seqlens is not None))
@@ -176,7 +182,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     W = _filter(weight, C, dev)
     _tensor(state, "state", dt, (B, W - 1, C), dev)
     _tensor(bias, "bias", _F32, (C,), dev, True)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
         out = call.new((B, C), dt)
     _tensor(out, "out", dt, (B, C), dev)
@@ -220,10 +226,11 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, Bm: t
     et, dev, shape = x.dtype, _device(x, "x"), x.shape
     _tensor(h0, "h0", _F32, (nseq, C, N), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
-        out = call.new(shape, et)
-    _tensor(out, "out", et, shape, dev)
+        out = call.like(x)
+    else:
+        _tensor(out, "out", et, shape, dev)
     if h_final is None and return_state:
         h_final = call.new((nseq, C, N), _F32)
     _tensor(h_final, "h_final", _F32, (nseq, C, N), dev, True)
@@ -251,12 +258,12 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B
     _tensor(h0, "h0", f32, (nseq, C, N), dev, True)
     _tensor(dh_final, "dh_final", f32, (nseq, C, N), dev, True)
     _tensor(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev, True)
-    call = _Call(dev, stream)
-    g = {"dx": call.new(shape, et), "ddt": call.new(shape, et), "dA_log": call.new((C, N), f32),
+    call = _Call(x, dev, stream)
+    g = {"dx": call.like(x), "ddt": call.like(x), "dA_log": call.new((C, N), f32),
          "dBm": call.new((*lead, G, N), et), "dCm": call.new((*lead, G, N), et),
          "dD": None if D is None else call.new((C,), f32),
          "ddt_bias": None if dt_bias is None else call.new((C,), f32),
-         "dz": None if z is None else call.new(shape, et),
+         "dz": None if z is None else call.like(x),
          "dh0": None if h0 is None else call.new((nseq, C, N), f32)}
     need = _cdr.library().comba_selective_scan_bwd_workspace_size(nseq, T, C, G, N, int(cu_seqlens is not None))
     ws = call.workspace(need, workspace)
@@ -279,7 +286,7 @@ def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, 
     dev = _device(x, "x")
     G, N = _scan_inputs((B,), C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
     _tensor(h, "h", _F32, (B, C, N), dev)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
         out = call.new((B, C), et)
     _tensor(out, "out", et, (B, C), dev)
@@ -305,10 +312,11 @@ def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: f
     _tensor(x, "x", dt, x.shape, dev)
     _tensor(gate, "gate", dt, x.shape, dev)
     _tensor(weight, "weight", _F32, (D,), dev)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
-        out = call.new(tuple(x.shape), dt)
-    _tensor(out, "out", dt, x.shape, dev)
+        out = call.like(x)
+    else:
+        _tensor(out, "out", dt, x.shape, dev)
     call("comba_gated_norm_fwd", x, gate, weight, out, rows, D, float(eps), _DTYPE[dt])
     return out
 
@@ -323,8 +331,8 @@ def gated_norm_bwd(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, do
     _tensor(gate, "gate", dt, x.shape, dev)
     _tensor(weight, "weight", _F32, (D,), dev)
     _tensor(dout, "dout", dt, x.shape, dev)
-    call = _Call(dev, stream)
-    g = {"dx": call.new(tuple(x.shape), dt), "dgate": call.new(tuple(x.shape), dt), "dweight": call.new((D,), _F32)}
+    call = _Call(x, dev, stream)
+    g = {"dx": call.like(x), "dgate": call.like(x), "dweight": call.new((D,), _F32)}
     ws = call.workspace(_cdr.library().comba_gated_norm_bwd_workspace_size(rows, D), workspace)
     call("comba_gated_norm_bwd", x, gate, weight, dout, g["dx"], g["dgate"], g["dweight"], rows, D, float(eps), _DTYPE[dt],
          ws, ws.numel())
@@ -353,13 +361,15 @@ def residual_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
     residual of x's dtype or fp32; weight, scale, post_weight [D] fp32 (the last two or
     None).  Returns (out like x, h like residual); ``h`` may be ``residual`` itself."""
     dt, rt, D, rows, dev = _residual_inputs(x, residual, "residual", weight, scale, post_weight)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     if out is None:
-        out = call.new(tuple(x.shape), dt)
-    _tensor(out, "out", dt, x.shape, dev)
+        out = call.like(x)
+    else:
+        _tensor(out, "out", dt, x.shape, dev)
     if h is None:
-        h = call.new(tuple(x.shape), rt)
-    _tensor(h, "h", rt, x.shape, dev)
+        h = call.like(residual)
+    else:
+        _tensor(h, "h", rt, x.shape, dev)
     call("comba_residual_norm_fwd", x, residual, weight, scale, post_weight, out, h, rows, D, float(eps), _DTYPE[dt],
          _DTYPE[rt])
     return out, h
@@ -375,9 +385,9 @@ def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dy
     dt, rt, D, rows, dev = _residual_inputs(x, h, "h", weight, scale, post_weight)
     _tensor(dy, "dy", dt, x.shape, dev)
     _tensor(dh, "dh", rt, x.shape, dev, True)
-    call = _Call(dev, stream)
+    call = _Call(x, dev, stream)
     f32 = _F32
-    g = {"dx": call.new(tuple(x.shape), dt), "dresidual": call.new(tuple(x.shape), rt), "dweight": call.new((D,), f32),
+    g = {"dx": call.like(x), "dresidual": call.like(h), "dweight": call.new((D,), f32),
          "dscale": None if scale is None else call.new((D,), f32),
          "dpost_weight": None if post_weight is None else call.new((D,), f32)}
     ws = call.workspace(_cdr.library().comba_residual_norm_bwd_workspace_size(rows, D), workspace)

@@ -84,10 +84,11 @@ int conv_bwd(conv::Params& p, float* dweight, float* dbias, bool silu, cudaStrea
 template <typename T, int W, int V>
 int conv_step(const T* x, const float* weight, const float* bias, T* state, T* out, int B, int C, bool silu,
               cudaStream_t s) {
-    const long blocks = ceil_div((long)B * (C / V), conv::kThreads);
+    const int cv = C / V, per = conv::step_sequences(B, cv);
+    const long blocks = ceil_div(ceil_div(B, per) * cv, conv::kThreads);
     if (blocks > kMaxGrid) return COMBA_EUNSUPPORTED;
-    if (silu) conv::step_kernel<T, W, V, true><<<(unsigned)blocks, conv::kThreads, 0, s>>>(x, weight, bias, state, out, B, C);
-    else conv::step_kernel<T, W, V, false><<<(unsigned)blocks, conv::kThreads, 0, s>>>(x, weight, bias, state, out, B, C);
+    if (silu) conv::step_kernel<T, W, V, true><<<(unsigned)blocks, conv::kThreads, 0, s>>>(x, weight, bias, state, out, B, C, per);
+    else conv::step_kernel<T, W, V, false><<<(unsigned)blocks, conv::kThreads, 0, s>>>(x, weight, bias, state, out, B, C, per);
     return launched();
 }
 
@@ -125,7 +126,7 @@ extern "C" int comba_short_conv_fwd(const void* x, const float* weight, const fl
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, out, final_state});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, out, final_state}) && aligned(weight, 16) && aligned(bias, 16);
     return COMBA_CONV_DISPATCH(conv_fwd, dtype, W, vec, p, silu != 0, s);
 }
 
@@ -162,7 +163,7 @@ extern "C" int comba_short_conv_bwd(const void* x, const float* weight, const fl
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, dout, dfinal_state, dx, dinitial_state});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, initial_state, dout, dfinal_state, dx, dinitial_state}) && aligned(weight, 16) && aligned(bias, 16);
     return COMBA_CONV_DISPATCH(conv_bwd, dtype, W, vec, p, dweight, dbias, silu != 0, s);
 }
 
@@ -178,7 +179,7 @@ extern "C" int comba_short_conv_step(const void* x, const float* weight, const f
     const Arg outs[] = {{state, nx * (W - 1), e, false}, {out, nx, e, false}};
     if (!args_ok(ins, outs)) return COMBA_EINVAL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, state, out});
+    const bool vec = vector_rows(C, conv::kChannels, conv::kChannels * e, {x, state, out}) && aligned(weight, 16) && aligned(bias, 16);
     const bool act = silu != 0;
     if (dtype == COMBA_BF16) {
         const auto* xt = static_cast<const bf16*>(x);
@@ -309,7 +310,7 @@ int scan_bwd(const scan::Params& p, cudaStream_t s) {
 
 template <typename T, int LPC>
 int scan_step(const scan::Params& p, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
+    const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)ceil_div(p.seq.N, scan::kStepSeqs));
     scan::step_kernel<T, LPC><<<grid, scan::kThreads, 0, s>>>(p);
     return launched();
 }

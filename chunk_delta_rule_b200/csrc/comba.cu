@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
@@ -705,10 +706,20 @@ int read_clear_status(cudaStream_t s) {
 
 }  // namespace
 
-// The status word's device address, for kernels of the library's other sources.
+// The status word's device address, for kernels of the library's other sources; found once
+// per device.
 int* comba::status_word() {
-    void* p = nullptr;
-    return cudaGetSymbolAddress(&p, comba::g_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+    static std::atomic<int*> known[kMaxDevices] = {};
+    int dev;
+    if (current_device(&dev)) return nullptr;
+    int* p = known[dev].load(std::memory_order_acquire);
+    if (!p) {
+        void* q = nullptr;
+        if (cudaGetSymbolAddress(&q, comba::g_status) != cudaSuccess) return nullptr;
+        p = static_cast<int*>(q);
+        known[dev].store(p, std::memory_order_release);
+    }
+    return p;
 }
 
 extern "C" int comba_get_last_error(void) {

@@ -77,13 +77,6 @@ __device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[NP / 2]) {
 __host__ __device__ inline long ckpt_slot(long s, int n, long k) { return s / kSub + n + k; }
 inline long ckpt_slots(const Seqs& q) { return q.tokens() / kSub + q.N + 1; }
 
-template <int LPC>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < LPC; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // Tokens of a tile, which a block stages in shared memory at a time, and the consecutive
 // channels of one token that a thread prepares: every thread has one such group a tile.
 __host__ __device__ constexpr int tile_tokens(int lpc) { return lpc < 8 ? 4 * lpc : 32; }
@@ -741,35 +734,53 @@ sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ 
     else if (dbias) dbias[i - C] = (float)v;
 }
 
-// One token: the state h [B, C, N] is read and written once.
+// One token: the state h [B, C, N] is read and written once, which bounds it.  A block takes
+// kStepSeqs sequences of its channels, all their loads in flight together.
+constexpr int kStepSeqs = 4;
 template <typename T, int LPC>
 __global__ void __launch_bounds__(kThreads)
 step_kernel(const __grid_constant__ Params p) {
-    constexpr int N = LPC * 4;
+    constexpr int N = 4 * LPC;
     const Place<LPC> at(p);
-    const int n = blockIdx.y;
-    float* hp = p.h_final + ((long)n * p.C + at.c) * N + at.n0;
-    float h[4], A[4], b[4], c[4];
-    load_v<4>(hp, h);
-    load_v<4>(p.A_log + (long)at.c * N + at.n0, A);
-    load_v<4>(static_cast<const T*>(p.Bm) + ((long)n * p.G + at.g) * N + at.n0, b);
-    load_v<4>(static_cast<const T*>(p.Cm) + ((long)n * p.G + at.g) * N + at.n0, c);
-    const long o = (long)n * p.C + at.c;
-    const float xv = to_f(static_cast<const T*>(p.x)[o]);
-    const float delta = softplus(to_f(static_cast<const T*>(p.dt)[o]) + (p.dt_bias ? p.dt_bias[at.c] : 0.f));
-    float y = 0.f;
+    if (!at.on) return;   // with all the lanes of its channel
+    const int first = blockIdx.y * kStepSeqs, count = min(p.seq.N - first, kStepSeqs);
+    const unsigned lanes = __activemask();
+    float h[kStepSeqs][4], b[kStepSeqs][4], c[kStepSeqs][4], x[kStepSeqs], dt[kStepSeqs], z[kStepSeqs];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(exp2_fast(delta * (-expf(A[i]) * kLog2e)), h[i], delta * xv * b[i]);
-        y = fmaf(h[i], c[i], y);
+    for (int k = 0; k < kStepSeqs; ++k) {
+        const long n = first + min(k, count - 1), o = n * p.C + at.c, g = (n * p.G + at.g) * N + at.n0;
+        load_v<4>(p.h_final + o * N + at.n0, h[k]);
+        load_v<4>(static_cast<const T*>(p.Bm) + g, b[k]);
+        load_v<4>(static_cast<const T*>(p.Cm) + g, c[k]);
+        x[k] = to_f(static_cast<const T*>(p.x)[o]);
+        dt[k] = to_f(static_cast<const T*>(p.dt)[o]);
+        z[k] = to_f(static_cast<const T*>(p.z ? p.z : p.x)[o]);
     }
-    y = lanes_sum<LPC>(y);
-    if (!at.on) return;
-    store_v<4>(hp, h);
-    if (at.n0 == 0) {
-        if (p.D) y = fmaf(p.D[at.c], xv, y);
-        if (p.z) y *= silu(to_f(static_cast<const T*>(p.z)[o]));
-        static_cast<T*>(p.out)[o] = from_f<T>(y);
+    Pair A2[2];
+    load_decays<LPC>(p, at, A2);
+    const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f, D = p.D ? p.D[at.c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kStepSeqs; ++k) {
+        if (k >= count) break;
+        const long o = (long)(first + k) * p.C + at.c;
+        const float delta = softplus(dt[k] + bias), u = delta * x[k];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float lo, hi;
+            const Pair a = exp2_pair(mul2(pair(delta, delta), A2[i]));
+            unpair(fma2(a, pair(h[k][2 * i], h[k][2 * i + 1]), mul2(pair(u, u), pair(b[k][2 * i], b[k][2 * i + 1]))), lo, hi);
+            h[k][2 * i] = lo;
+            h[k][2 * i + 1] = hi;
+            y = fmaf(lo, c[k][2 * i], fmaf(hi, c[k][2 * i + 1], y));
+        }
+        store_v<4>(p.h_final + o * N + at.n0, h[k]);
+#pragma unroll
+        for (int w = 1; w < LPC; w *= 2) y += __shfl_xor_sync(lanes, y, w);
+        if (at.n0 == 0) {
+            y = fmaf(D, x[k], y);
+            static_cast<T*>(p.out)[o] = from_f<T>(p.z ? y * silu(z[k]) : y);
+        }
     }
 }
 

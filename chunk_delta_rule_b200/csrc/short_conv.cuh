@@ -35,13 +35,21 @@ struct Params {
     int* status;
 };
 
+// The filters and biases of channels c .. c+V-1 (V == 4: their V W weights are 16-byte aligned).
 template <int W, int V>
-__device__ __forceinline__ void load_filter(const Params& p, int c, float (&w)[W][V], float (&b)[V]) {
+__device__ __forceinline__ void load_filter(const float* __restrict__ weight, const float* __restrict__ bias, int c,
+                                            float (&w)[W][V], float (&b)[V]) {
+    float f[V * W];
+    load_v<V * W>(weight + (long)c * W, f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = p.weight[(long)(c + i) * W + j];
-        b[i] = p.bias ? p.bias[c + i] : 0.f;
+        for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
+    if (bias) {
+        load_v<V>(bias + c, b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = 0.f;
     }
 }
 
@@ -130,7 +138,7 @@ fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
     R ring{mem};
     const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
     float w[W][V], b[V];
-    load_filter<W, V>(p, c, w, b);
+    load_filter<W, V>(p.weight, p.bias, c, w, b);
     long t = t0;
     for (int n = p.seq.find(t0); n < p.seq.N && t < t1; ++n) {
         long s, e;
@@ -212,7 +220,7 @@ bwd_state_kernel(const __grid_constant__ Params p, long total) {
     }
     if (!p.dinit) return;
     float w[W][V], b[V], g[V];
-    load_filter<W, V>(p, c, w, b);
+    load_filter<W, V>(p.weight, p.bias, c, w, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] = 0.f;
     const long at = m - (e - s);   // its row of the final state, of a sequence shorter than that
@@ -249,7 +257,7 @@ bwd_kernel(const __grid_constant__ Params p, long total) {
     __shared__ typename R::Storage mem;
     R ring{mem};
     float w[W][V], b[V];
-    load_filter<W, V>(p, c, w, b);
+    load_filter<W, V>(p.weight, p.bias, c, w, b);
     const long t0 = row * p.L, t1 = min(t0 + (long)p.L, p.seq.tokens());
     float dw[W][V], db[V];
 #pragma unroll
@@ -373,36 +381,51 @@ sum_kernel(const float* __restrict__ part, float* __restrict__ dweight, float* _
     else if (dbias) dbias[c] = (float)acc;
 }
 
-// One token: out = silu(bias + sum_j w_j [state, x]_j), and the state moves on by x.
+// One token: out = silu(bias + sum_j w_j [state, x]_j), and the state moves on by x.  A thread
+// takes `per` sequences of its channels, kStepSeqs of them in flight, for one load of the
+// filter.
+constexpr int kStepSeqs = 4;
 template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads)
 step_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
-            T* state, T* __restrict__ out, long B, int C) {
+            T* state, T* __restrict__ out, int B, int C, int per) {
     const long id = (long)blockIdx.x * kThreads + threadIdx.x;
     const int cv = C / V;
-    const long n = id / cv;
-    if (n >= B) return;
-    const int c = (int)(id - n * cv) * V;
-    Params p{};
-    p.weight = weight;
-    p.bias = bias;
-    float w[W][V], b[V], h[W][V];
+    const long n0 = id / cv * per;
+    if (n0 >= B) return;
+    const int c = (int)(id % cv) * V, end = (int)min(n0 + per, (long)B);
+    float w[W][V], b[V];
+    load_filter<W, V>(weight, bias, c, w, b);
+#pragma unroll 1
+    for (int n = (int)n0; n < end; n += kStepSeqs) {
+        float h[kStepSeqs][W][V];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_v<V>(state + (n * (W - 1) + j) * C + c, h[j]);
-    load_v<V>(x + n * C + c, h[W - 1]);
-    load_filter<W, V>(p, c, w, b);
-    float y[V];
+        for (int k = 0; k < kStepSeqs; ++k) {
+            const long m = min(n + k, end - 1);   // the last one again where there are fewer
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        y[i] = b[i];
+            for (int j = 0; j < W - 1; ++j) load_v<V>(state + (m * (W - 1) + j) * C + c, h[k][j]);
+            load_v<V>(x + m * C + c, h[k][W - 1]);
+        }
 #pragma unroll
-        for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], h[j][i], y[i]);
-        if (SILU) y[i] = silu(y[i]);
+        for (int k = 0; k < kStepSeqs; ++k) {
+            if (n + k >= end) break;
+            const long m = n + k;
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = b[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) fma_v<V>(w[j], h[k][j], y);
+            if (SILU)
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
+            store_v<V>(out + m * C + c, y);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) store_v<V>(state + (m * (W - 1) + j) * C + c, h[k][j + 1]);
+        }
     }
-    store_v<V>(out + n * C + c, y);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_v<V>(state + (n * (W - 1) + j) * C + c, h[j + 1]);
 }
+// Sequences a thread takes: kStepSeqs once that still leaves an SM 512 threads.
+inline int step_sequences(long B, int cv) { return B * cv >= (long)kSMs * 512 * kStepSeqs ? kStepSeqs : 1; }
 
 // Tokens in a tile: long tiles read fewer tokens twice (W-1 a tile) and, in the backward,
 // write fewer partial sums; short ones give enough threads when the tokens are few.
