@@ -206,17 +206,17 @@ namespace {
 
 bool states_ok(int N) { return N == 8 || N == 16 || N == 32 || N == 64 || N == 128; }
 
-// Whether groups of consecutive channels lie whole and aligned in every token tensor.
-bool scan_vector(int C, int G, int N, int dtype, std::initializer_list<const void*> ptrs) {
-    const int e = scan::group_channels(N / 4);
-    if (C / G % e) return false;
+// Whether groups of up to 4 consecutive channels lie whole and aligned in every token tensor.
+bool scan_vector(int C, int G, int dtype, std::initializer_list<const void*> ptrs) {
+    if (C / G % 4) return false;
     for (const void* p : ptrs)
-        if (!aligned(p, e * elt_size(dtype))) return false;
+        if (!aligned(p, 4 * elt_size(dtype))) return false;
     return true;
 }
 
 // Channel blocks of one group.
-int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, scan::kThreads / (N / 4)); }
+int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, 4 * scan::Layout<16>::NT / N); }
+
 
 struct ScanWs {
     size_t ckpt, bc, a, d, total;   // byte offsets
@@ -270,48 +270,48 @@ SplitWs split_ws(const Seqs& q, int C, int G, int N) {
     return w;
 }
 
-template <typename T, int LPC>
+template <typename T, class K>
 int scan_fwd(const scan::Params& p, cudaStream_t s) {
     const unsigned bx = (unsigned)(p.G * group_blocks(p.C, p.G, p.N));
     if (p.pieces > 1) {
         const dim3 grid(bx, (unsigned)p.pieces);
         if (p.vec) {
-            scan::ends_kernel<T, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
-            scan::split_kernel<T, LPC, true><<<grid, scan::kThreads, 0, s>>>(p);
+            scan::ends_kernel<T, K, true><<<grid, K::NT, 0, s>>>(p);
+            scan::split_kernel<T, K, true><<<grid, K::NT, 0, s>>>(p);
         } else {
-            scan::ends_kernel<T, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
-            scan::split_kernel<T, LPC, false><<<grid, scan::kThreads, 0, s>>>(p);
+            scan::ends_kernel<T, K, false><<<grid, K::NT, 0, s>>>(p);
+            scan::split_kernel<T, K, false><<<grid, K::NT, 0, s>>>(p);
         }
         return launched();
     }
     const dim3 grid(bx, (unsigned)p.seq.N);
-    if (p.vec) scan::fwd_kernel<T, LPC, scan::kOutputs, true><<<grid, scan::kThreads, 0, s>>>(p);
-    else scan::fwd_kernel<T, LPC, scan::kOutputs, false><<<grid, scan::kThreads, 0, s>>>(p);
+    if (p.vec) scan::fwd_kernel<T, K, scan::kOutputs, true><<<grid, K::NT, 0, s>>>(p);
+    else scan::fwd_kernel<T, K, scan::kOutputs, false><<<grid, K::NT, 0, s>>>(p);
     return launched();
 }
 
-template <typename T, int LPC>
+template <typename T, class K>
 int scan_bwd(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    if (p.vec) scan::fwd_kernel<T, LPC, scan::kStates, true><<<grid, scan::kThreads, 0, s>>>(p);
-    else scan::fwd_kernel<T, LPC, scan::kStates, false><<<grid, scan::kThreads, 0, s>>>(p);
-    constexpr int smem = (int)sizeof(scan::BwdSmem<LPC>);
+    if (p.vec) scan::fwd_kernel<T, K, scan::kStates, true><<<grid, K::NT, 0, s>>>(p);
+    else scan::fwd_kernel<T, K, scan::kStates, false><<<grid, K::NT, 0, s>>>(p);
+    constexpr int smem = (int)sizeof(scan::BwdSmem<K>);
     if (p.vec) {
-        if (cudaFuncSetAttribute(scan::bwd_kernel<T, LPC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        if (cudaFuncSetAttribute(scan::bwd_kernel<T, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return COMBA_ECUDA;
-        scan::bwd_kernel<T, LPC, true><<<grid, scan::kThreads, smem, s>>>(p);
+        scan::bwd_kernel<T, K, true><<<grid, K::NT, smem, s>>>(p);
     } else {
-        if (cudaFuncSetAttribute(scan::bwd_kernel<T, LPC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        if (cudaFuncSetAttribute(scan::bwd_kernel<T, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return COMBA_ECUDA;
-        scan::bwd_kernel<T, LPC, false><<<grid, scan::kThreads, smem, s>>>(p);
+        scan::bwd_kernel<T, K, false><<<grid, K::NT, smem, s>>>(p);
     }
     return launched();
 }
 
-template <typename T, int LPC>
+template <typename T, class K>
 int scan_step(const scan::Params& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)ceil_div(p.seq.N, scan::kStepSeqs));
-    scan::step_kernel<T, LPC><<<grid, scan::kThreads, 0, s>>>(p);
+    scan::step_kernel<T, K><<<grid, K::NT, 0, s>>>(p);
     return launched();
 }
 
@@ -327,11 +327,13 @@ int scan_sums(const scan::Params& p, void* dB, void* dC, float* dA_log, float* d
     return launched();
 }
 
-#define COMBA_SCAN_LPC(f, T, N, ...)                                                                         \
-    ((N) == 8 ? f<T, 2>(__VA_ARGS__) : (N) == 16 ? f<T, 4>(__VA_ARGS__)    \
-     : (N) == 32 ? f<T, 8>(__VA_ARGS__) : (N) == 64 ? f<T, 16>(__VA_ARGS__) : f<T, 32>(__VA_ARGS__))
+// f<element type, layout> for the runtime values.
+#define COMBA_SCAN_N(f, T, N, ...)                                                                                \
+    ((N) == 8 ? f<T, scan::Layout<8>>(__VA_ARGS__) : (N) == 16 ? f<T, scan::Layout<16>>(__VA_ARGS__)              \
+     : (N) == 32 ? f<T, scan::Layout<32>>(__VA_ARGS__) : (N) == 64 ? f<T, scan::Layout<64>>(__VA_ARGS__)          \
+                                                                   : f<T, scan::Layout<128>>(__VA_ARGS__))
 #define COMBA_SCAN_DISPATCH(f, dtype, N, ...) \
-    ((dtype) == COMBA_BF16 ? COMBA_SCAN_LPC(f, bf16, N, __VA_ARGS__) : COMBA_SCAN_LPC(f, float, N, __VA_ARGS__))
+    ((dtype) == COMBA_BF16 ? COMBA_SCAN_N(f, bf16, N, __VA_ARGS__) : COMBA_SCAN_N(f, float, N, __VA_ARGS__))
 
 // Sizes of a scan: COMBA_OK, or why it is refused.
 int scan_sizes(int nseq, int T, int C, int G, int N, int dtype, size_t tokens) {
@@ -375,7 +377,7 @@ extern "C" int comba_selective_scan_fwd(const void* x, const void* dt, const flo
     p.out = out; p.h_final = h_final;
     p.seq = seq;
     p.C = C; p.G = G; p.N = N;
-    p.vec = scan_vector(C, G, N, dtype, {x, dt, z, out});
+    p.vec = scan_vector(C, G, dtype, {x, dt, z, out});
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     p.piece = ws.piece;
@@ -424,7 +426,7 @@ extern "C" int comba_selective_scan_bwd(const void* x, const void* dt, const flo
     p.dout = dout; p.dh_final = dh_final; p.dx = dx; p.ddt = ddt; p.dz = dz; p.dh0 = dh0;
     p.seq = Seqs{cu_seqlens, nseq, T};
     p.C = C; p.G = G; p.N = N;
-    p.vec = scan_vector(C, G, N, dtype, {x, dt, z, dout, dx, ddt, dz});
+    p.vec = scan_vector(C, G, dtype, {x, dt, z, dout, dx, ddt, dz});
     char* w = static_cast<char*>(workspace);
     const ScanWs ws = scan_ws(p.seq, C, G, N);
     p.ckpt = reinterpret_cast<float*>(w + ws.ckpt);

@@ -5,8 +5,8 @@
 //   h_t = a h_{t-1} + delta x_t B_t,   y_t = sum_n h_t C_t + D x_t,   out_t = y_t silu(z_t)
 //
 // (the discretisation of comba_chunk_fwd_gated, per channel and state entry instead of per
-// head).  A thread holds 4 neighbouring entries of one channel's state in registers and
-// N / 4 neighbouring lanes hold a channel.
+// head).  A thread holds 4 neighbouring entries of one channel's state in registers, and
+// neighbouring lanes hold a channel.
 #pragma once
 
 #include "block_common.cuh"
@@ -16,7 +16,6 @@ namespace scan {
 
 using namespace blk;
 
-constexpr int kThreads = 128;
 constexpr int kBatch = 4;        // tokens whose operands a lane holds at a time
 constexpr int kSub = 8;          // tokens between two stored states of the backward
 
@@ -44,31 +43,14 @@ __device__ __forceinline__ Pair exp2_pair(Pair v) {
     unpair(v, a, b);
     return pair(exp2_fast(a), exp2_fast(b));
 }
-// NP / 2 pairs at p (16-byte aligned for NP >= 4).
-template <int NP>
-__device__ __forceinline__ void load_pairs(const float* p, Pair (&v)[NP / 2]) {
-    if constexpr (NP % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) {
-            const ulonglong2 u = reinterpret_cast<const ulonglong2*>(p)[i];
-            v[2 * i] = u.x;
-            v[2 * i + 1] = u.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) v[i] = reinterpret_cast<const Pair*>(p)[i];
-    }
+// Two pairs at p, 16-byte aligned.
+__device__ __forceinline__ void load_pairs(const float* p, Pair (&v)[2]) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = u.x;
+    v[1] = u.y;
 }
-
-template <int NP>
-__device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[NP / 2]) {
-    if constexpr (NP % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) reinterpret_cast<ulonglong2*>(p)[i] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) reinterpret_cast<Pair*>(p)[i] = v[i];
-    }
+__device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[2]) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
 }
 
 // Slot of the stored state of sub-chunk k of sequence n that starts at token s: a sequence
@@ -77,10 +59,19 @@ __device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[NP / 2]) {
 __host__ __device__ inline long ckpt_slot(long s, int n, long k) { return s / kSub + n + k; }
 inline long ckpt_slots(const Seqs& q) { return q.tokens() / kSub + q.N + 1; }
 
-// Tokens of a tile, which a block stages in shared memory at a time, and the consecutive
-// channels of one token that a thread prepares: every thread has one such group a tile.
-__host__ __device__ constexpr int tile_tokens(int lpc) { return lpc < 8 ? 4 * lpc : 32; }
-__host__ __device__ constexpr int group_channels(int lpc) { return tile_tokens(lpc) / lpc; }
+// How the kernels lay out N state entries: NP a lane, LPC lanes a channel, NT threads a block
+// (CB channels), and tiles of TT tokens, which a block stages in shared memory at a time.
+// Every thread prepares one group of E consecutive channels of one token of a tile.
+// Measured for N = 16, forward of B8 T4096 C2048: NP 2, 4, 8 take 668, 571, 676 us (more lanes
+// repeat the operands' reads, fewer leave too few warps); NT 64, 128, 256 take 571, 571, 614 us,
+// and 2.80, 1.79, 1.86 ms over 64K tokens of one sequence.  The backward prefers the same.
+template <int N_>
+struct Layout {
+    static constexpr int N = N_, NP = 4, PP = NP / 2, LPC = N / NP, NT = 128, TT = N < 32 ? N : N < 128 ? 16 : 32;
+    static constexpr int CB = NT / LPC, E = TT / LPC;
+    static constexpr int YL = LPC < 4 ? LPC : 4;   // partial sums of a channel, each of LPC / YL lanes
+    static_assert(E * LPC == TT && (E == 1 || E == 2 || E == 4) && CB % E == 0 && TT % 8 == 0, "one group a thread");
+};
 
 // E consecutive elements.  VEC: as one access (all such groups are whole and aligned), else
 // one by one, those past the first `count` from the first one's place.  Loads carry no
@@ -129,49 +120,53 @@ __device__ __forceinline__ void widen(uint2 r, float (&v)[4]) {
 
 // A thread's two places in a block: a lane of the scan (channel c, entries n0 .. n0+3), and
 // the preparer of the channels gc .. gc+E-1 (of which `count` exist) of token gt of a tile.
-template <int LPC>
+template <class K>
 struct Place {
-    static constexpr int CB = kThreads / LPC, TT = tile_tokens(LPC), E = group_channels(LPC);
     int g, c, n0, li;      // group, channel, entry, channel within the block
     bool on;
     int gt, gi, gc, count; // token of the tile, channel within the block, channel
     __device__ __forceinline__ Place(const Params& p) {
-        const int tid = threadIdx.x, cpg = p.C / p.G, bpg = (cpg + CB - 1) / CB;
+        const int tid = threadIdx.x, cpg = p.C / p.G, bpg = (cpg + K::CB - 1) / K::CB;
         g = blockIdx.x / bpg;
-        const int c0 = (blockIdx.x % bpg) * CB;
-        li = tid / LPC;
-        n0 = tid % LPC * 4;
+        const int c0 = (blockIdx.x % bpg) * K::CB;
+        li = tid / K::LPC;
+        n0 = tid % K::LPC * K::NP;
         on = c0 + li < cpg;
         c = g * cpg + (on ? c0 + li : 0);
-        gt = tid / (CB / E);
-        gi = tid % (CB / E) * E;
-        count = min(max(cpg - c0 - gi, 0), E);
+        gt = tid / (K::CB / K::E);
+        gi = tid % (K::CB / K::E) * K::E;
+        count = min(max(cpg - c0 - gi, 0), K::E);
         gc = g * cpg + (count > 0 ? c0 + gi : 0);
     }
 };
 
-template <int LPC>
+template <class K>
 struct FwdSmem {
-    static constexpr int N = 4 * LPC, CB = kThreads / LPC, TT = tile_tokens(LPC);
-    float2 du[TT][CB];                 // delta, delta x
-    alignas(16) float bc[2][TT][N];
-    // partial sums of the lanes (of pairs of them where they are 32, to fit 48 KB)
-    static constexpr int YL = LPC < 32 ? LPC : 16;
-    alignas(16) float y[TT][CB][YL];
+    float2 du[K::TT][K::CB];                 // delta, delta x
+    alignas(16) float bc[2][K::TT][K::N];
+    alignas(16) float y[K::TT][K::CB][K::YL];   // a channel's partial sums, of up to 4 sets of its lanes
 };
 
-// Where channel `ch` of token t lies in a row of du and of y: permuted within four
-// neighbours, so that the preparers (4 channels a thread) and the lanes (one channel each)
-// both touch different banks (for 8 to 32 lanes a channel, y's reads keep conflicts).
-template <int LPC>
+// Where channel `ch` of token t lies in a row of du, and in one of partial sums: permuted
+// among its group, so that the preparers (a group a thread) and the lanes (a channel each)
+// both touch different banks.
+template <class K>
 __device__ __forceinline__ int du_slot(int t, int ch) {
-    return group_channels(LPC) == 4 ? ch ^ (((ch >> 4) & 1) | ((t & 1) << 1)) : ch;
+    return K::E == 4 ? ch ^ (((ch >> 4) & 1) | ((t & 1) << 1)) : K::E == 2 ? ch ^ ((ch >> 4) & 1) : ch;
 }
-// LPC: the partial sums of a channel
-template <int LPC>
+template <class K>
 __device__ __forceinline__ int y_slot(int ch) {
-    return group_channels(LPC) == 4 ? ch ^ ((ch >> (LPC == 2 ? 4 : LPC == 4 ? 3 : 2)) & 3) : ch;
+    return K::E == 4 ? ch ^ ((ch >> (K::YL == 2 ? 4 : 3)) & 3) : K::E == 2 ? ch ^ ((ch >> 3) & 1) : ch;
 }
+// Sums v over the lanes of a channel that share one of its YL partial sums.
+template <class K>
+__device__ __forceinline__ float set_sum(float v) {
+#pragma unroll
+    for (int o = K::LPC / K::YL / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <class K>
+__device__ __forceinline__ int set_of(int tid) { return tid % K::LPC / (K::LPC / K::YL); }
 
 enum Mode {
     kOutputs,   // out
@@ -187,13 +182,13 @@ enum Mode {
 // shared memory.  (2) The lanes walk the tile's tokens, with only the state's own chain
 // between them.  (3) The first phase's thread sums y over the lanes, adds D x, applies the
 // gate and stores.  The next tile's loads are in flight during (2).
-template <typename T, int LPC, Mode M, bool VEC>
-__device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Place<LPC>& at, int n, long s, long from,
-                                     long to, const Pair (&A2)[2], Pair (&h)[2], float& dsum) {
-    constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E;
-    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;   // of B and C
+template <typename T, class K, Mode M, bool VEC>
+__device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Place<K>& at, int n, long s, long from,
+                                     long to, const Pair (&A2)[K::PP], Pair (&h)[K::PP], float& dsum) {
+    constexpr int N = K::N, TT = K::TT, E = K::E, PP = K::PP;
+    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + K::NT - 1) / K::NT;   // of B and C
     if (from >= to) return;   // fetch() needs a last token to clamp to
-    const int tid = threadIdx.x, ys = y_slot<LPC>(at.li);
+    const int tid = threadIdx.x, ys = y_slot<K>(at.li);
     float bias[E], D[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -214,7 +209,7 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         if (gated) prefetch_l2(static_cast<const T*>(p.z) + ahead);
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * kThreads, r = q % QUADS;
+            const int q = tid + k * K::NT, r = q % QUADS;
             const long tb = min(t0 + r / (N / 4), to - 1);
             br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
                 static_cast<const T*>(M == kOutputs && q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
@@ -228,11 +223,11 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         for (int i = 0; i < E; ++i) {
             // past the end: delta = 0 and delta x = 0 leave the state as it is
             const float delta = softplus(to_f(dr.v[i]) + bias[i]);
-            sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)] = live ? make_float2(delta, delta * to_f(x.v[i])) : make_float2(0.f, 0.f);
+            sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)] = live ? make_float2(delta, delta * to_f(x.v[i])) : make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * kThreads;
+            const int q = tid + k * K::NT;
             float v[4];
             widen(br[k], v);
             const bool in = t0 + q % QUADS / (N / 4) < to;
@@ -245,58 +240,61 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
         // kBatch tokens at a time: their operands are read, and their decays and inputs formed,
         // before the previous batch's y is stored (a store would hold back later loads)
         float2 du[kBatch];
-        Pair b[kBatch][2], c[kBatch][2];
+        Pair b[kBatch][PP], c[kBatch][PP];
         auto operands = [&](int j0) {
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                du[j] = sm.du[j0 + j][du_slot<LPC>(j0 + j, at.li)];
-                load_pairs<4>(&sm.bc[0][j0 + j][at.n0], b[j]);
+                du[j] = sm.du[j0 + j][du_slot<K>(j0 + j, at.li)];
+                load_pairs(&sm.bc[0][j0 + j][at.n0], b[j]);
             }
         };
         operands(0);
 #pragma unroll
         for (int j0 = 0; j0 < TT; j0 += kBatch) {
-            Pair a[kBatch][2];
+            Pair a[kBatch][PP];
             float y[kBatch], dl[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 dl[j] = du[j].x;
                 const Pair d2 = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < PP; ++i) {
                     a[j][i] = exp2_pair(mul2(d2, A2[i]));
                     b[j][i] = mul2(u, b[j][i]);
                 }
-                if (M == kOutputs) load_pairs<4>(&sm.bc[1][j0 + j][at.n0], c[j]);
+                if (M == kOutputs) load_pairs(&sm.bc[1][j0 + j][at.n0], c[j]);
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (M == kStates && (j0 + j) % kSub == 0 && at.on && t0 + j0 + j < to)
-                    store_pairs<4>(p.ckpt + (ckpt_slot(s, n, (t0 - s + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
-                h[0] = fma2(a[j][0], h[0], b[j][0]);
-                h[1] = fma2(a[j][1], h[1], b[j][1]);
+                    store_pairs(p.ckpt + (ckpt_slot(s, n, (t0 - s + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
+                Pair acc;
+#pragma unroll
+                for (int i = 0; i < PP; ++i) {
+                    h[i] = fma2(a[j][i], h[i], b[j][i]);
+                    if (M == kOutputs) acc = i ? fma2(h[i], c[j][i], acc) : mul2(h[i], c[j][i]);
+                }
                 if (M == kEnds) dsum += dl[j];
                 if (M == kOutputs) {
                     float lo, hi;
-                    unpair(fma2(h[1], c[j][1], mul2(h[0], c[j][0])), lo, hi);
-                    y[j] = lo + hi;
-                    if (LPC > FwdSmem<LPC>::YL) y[j] += __shfl_xor_sync(0xffffffffu, y[j], 1);
+                    unpair(acc, lo, hi);
+                    y[j] = set_sum<K>(lo + hi);
                 }
             }
             if (j0 + kBatch < TT) operands(j0 + kBatch);
             if (M == kOutputs)
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) sm.y[j0 + j][ys][tid % LPC / (LPC / FwdSmem<LPC>::YL)] = y[j];
+                for (int j = 0; j < kBatch; ++j) sm.y[j0 + j][ys][set_of<K>(tid)] = y[j];
         }
         __syncthreads();
         if (M == kOutputs && live && at.count > 0) {
             float y[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float* l = sm.y[at.gt][y_slot<LPC>(at.gi + i)];
+                const float* l = sm.y[at.gt][y_slot<K>(at.gi + i)];
                 y[i] = l[0] + l[1];
 #pragma unroll
-                for (int k = 2; k < FwdSmem<LPC>::YL; k += 2) y[i] += l[k] + l[k + 1];
+                for (int k = 2; k < K::YL; k += 2) y[i] += l[k] + l[k + 1];
                 y[i] = fmaf(D[i], to_f(x.v[i]), y[i]);
                 if (gated) y[i] *= silu(to_f(z.v[i]));
             }
@@ -305,33 +303,33 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<LPC>& sm, const Pl
     }
 }
 
-template <int LPC>
-__device__ __forceinline__ void load_decays(const Params& p, const Place<LPC>& at, Pair (&A2)[2]) {
-    float a[4];
-    load_v<4>(p.A_log + (long)at.c * (4 * LPC) + at.n0, a);
+template <class K>
+__device__ __forceinline__ void load_decays(const Params& p, const Place<K>& at, Pair (&A2)[K::PP]) {
+    float a[K::NP];
+    load_v<K::NP>(p.A_log + (long)at.c * K::N + at.n0, a);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) A2[i] = pair(-expf(a[2 * i]) * kLog2e, -expf(a[2 * i + 1]) * kLog2e);
+    for (int i = 0; i < K::PP; ++i) A2[i] = pair(-expf(a[2 * i]) * kLog2e, -expf(a[2 * i + 1]) * kLog2e);
 }
 
 // One block per (channel block, sequence).
-template <typename T, int LPC, Mode M, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class K, Mode M, bool VEC>
+__global__ void __launch_bounds__(K::NT)
 fwd_kernel(const __grid_constant__ Params p) {
-    __shared__ FwdSmem<LPC> sm;
-    const Place<LPC> at(p);
+    __shared__ FwdSmem<K> sm;
+    const Place<K> at(p);
     const int n = blockIdx.y;
     long s, e;
     if (!p.seq.bounds(n, s, e)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
         return;
     }
-    const long hrow = ((long)n * p.C + at.c) * (4 * LPC) + at.n0;
-    Pair A2[2], h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    const long hrow = ((long)n * p.C + at.c) * K::N + at.n0;
+    Pair A2[K::PP], h[K::PP] = {};
     float dsum;
-    load_decays<LPC>(p, at, A2);
-    if (p.h0) load_pairs<4>(p.h0 + hrow, h);
-    walk<T, LPC, M, VEC>(p, sm, at, n, s, s, e, A2, h, dsum);
-    if (M == kOutputs && p.h_final && at.on) store_pairs<4>(p.h_final + hrow, h);
+    load_decays<K>(p, at, A2);
+    if (p.h0) load_pairs(p.h0 + hrow, h);
+    walk<T, K, M, VEC>(p, sm, at, n, s, s, e, A2, h, dsum);
+    if (M == kOutputs && p.h_final && at.on) store_pairs(p.h_final + hrow, h);
 }
 
 // The split form, for too few (channel block, sequence) pairs to fill the GPU: the joint
@@ -340,48 +338,48 @@ fwd_kernel(const __grid_constant__ Params p) {
 //
 // First sweep: for a piece that ends inside a sequence, r from that sequence's tokens in it
 // (from h0 where the sequence starts there, so that r is the state itself) and sum delta.
-template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class K, bool VEC>
+__global__ void __launch_bounds__(K::NT)
 ends_kernel(const __grid_constant__ Params p) {
-    __shared__ FwdSmem<LPC> sm;
-    const Place<LPC> at(p);
+    __shared__ FwdSmem<K> sm;
+    const Place<K> at(p);
     const long t0 = blockIdx.y * p.piece, t1 = min(t0 + p.piece, p.seq.tokens());
     const int n = p.seq.find(t1 - 1);
     long s, e;
     if (!p.seq.bounds(n, s, e) || s >= t1 || e <= t1) return;
-    Pair A2[2], h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    Pair A2[K::PP], h[K::PP] = {};
     float dsum = 0.f;
-    load_decays<LPC>(p, at, A2);
-    if (s >= t0 && p.h0) load_pairs<4>(p.h0 + ((long)n * p.C + at.c) * (4 * LPC) + at.n0, h);
-    walk<T, LPC, kEnds, VEC>(p, sm, at, n, s, max(s, t0), t1, A2, h, dsum);
+    load_decays<K>(p, at, A2);
+    if (s >= t0 && p.h0) load_pairs(p.h0 + ((long)n * p.C + at.c) * K::N + at.n0, h);
+    walk<T, K, kEnds, VEC>(p, sm, at, n, s, max(s, t0), t1, A2, h, dsum);
     if (!at.on) return;
     const long row = (long)blockIdx.y * p.C + at.c;
-    store_pairs<4>(p.ends + row * (4 * LPC) + at.n0, h);
+    store_pairs(p.ends + row * K::N + at.n0, h);
     if (at.n0 == 0) p.dsum[row] = dsum;
 }
 
 // Second sweep: every piece again, each sequence in it from its start state, which the
 // block composes from the pieces before it.
-template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class K, bool VEC>
+__global__ void __launch_bounds__(K::NT)
 split_kernel(const __grid_constant__ Params p) {
-    constexpr int N = 4 * LPC;
-    __shared__ FwdSmem<LPC> sm;
-    const Place<LPC> at(p);
+    constexpr int N = K::N;
+    __shared__ FwdSmem<K> sm;
+    const Place<K> at(p);
     const int j = blockIdx.y;
     for (int n = j; n < p.seq.N; n += p.pieces) {   // sequences without tokens, and bad bounds
         long s, e;
         const bool ok = p.seq.bounds(n, s, e);
         if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
         if (!ok || s < e || !p.h_final || !at.on) continue;
-        Pair h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        Pair h[K::PP] = {};
         const long hrow = ((long)n * p.C + at.c) * N + at.n0;
-        if (p.h0) load_pairs<4>(p.h0 + hrow, h);
-        store_pairs<4>(p.h_final + hrow, h);
+        if (p.h0) load_pairs(p.h0 + hrow, h);
+        store_pairs(p.h_final + hrow, h);
     }
-    Pair A2[2];
+    Pair A2[K::PP];
     float dsum;
-    load_decays<LPC>(p, at, A2);
+    load_decays<K>(p, at, A2);
     const long t0 = j * p.piece, t1 = min(t0 + p.piece, p.seq.tokens());
     long t = t0;
     for (int n = p.seq.find(t0); n < p.seq.N && t < t1; ++n) {
@@ -390,24 +388,24 @@ split_kernel(const __grid_constant__ Params p) {
         if (s >= t1) break;
         t = max(t, s);
         const long hrow = ((long)n * p.C + at.c) * N + at.n0, stop = min(e, t1);
-        Pair h[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        Pair h[K::PP] = {};
         if (t == s) {
-            if (p.h0) load_pairs<4>(p.h0 + hrow, h);
+            if (p.h0) load_pairs(p.h0 + hrow, h);
         } else {
             const int j0 = (int)(s / p.piece);
-            load_pairs<4>(p.ends + ((long)j0 * p.C + at.c) * N + at.n0, h);
+            load_pairs(p.ends + ((long)j0 * p.C + at.c) * N + at.n0, h);
 #pragma unroll 4
             for (int i = j0 + 1; i < j; ++i) {
                 const long row = (long)i * p.C + at.c;
                 const float ds = p.dsum[row];
-                Pair r[2];
-                load_pairs<4>(p.ends + row * N + at.n0, r);
-                h[0] = fma2(exp2_pair(mul2(pair(ds, ds), A2[0])), h[0], r[0]);
-                h[1] = fma2(exp2_pair(mul2(pair(ds, ds), A2[1])), h[1], r[1]);
+                Pair r[K::PP];
+                load_pairs(p.ends + row * N + at.n0, r);
+#pragma unroll
+                for (int k = 0; k < K::PP; ++k) h[k] = fma2(exp2_pair(mul2(pair(ds, ds), A2[k])), h[k], r[k]);
             }
         }
-        walk<T, LPC, kOutputs, VEC>(p, sm, at, n, s, t, stop, A2, h, dsum);
-        if (stop == e && p.h_final && at.on) store_pairs<4>(p.h_final + hrow, h);
+        walk<T, K, kOutputs, VEC>(p, sm, at, n, s, t, stop, A2, h, dsum);
+        if (stop == e && p.h_final && at.on) store_pairs(p.h_final + hrow, h);
         t = stop;
     }
 }
@@ -423,63 +421,64 @@ split_kernel(const __grid_constant__ Params p) {
 // y, du and ddelta's first part are summed over a channel's lanes by the preparers.  dB and
 // dC are summed over a warp's channels by halving shuffles, over the block's warps through
 // shared memory, and leave one row per channel block.
-constexpr int kWarps = kThreads / 32;
 constexpr int kFlush = 16;
+constexpr int kBwdBlocks = 2;   // that an SM's registers hold: 3 would spill, and took 774 us for 732 (B8 T2048 C1024)
 
-template <int LPC>
+template <class K>
 struct BwdSmem {
-    static constexpr int N = 4 * LPC, CB = kThreads / LPC, TT = tile_tokens(LPC), YL = LPC < 4 ? LPC : 4;
-    float2 du[TT][CB];                       // delta, delta x
-    alignas(16) float dy[TT][CB];
-    alignas(16) float bc[2][TT][N];
-    alignas(16) float part[3][TT][CB][YL];   // partial sums of y, du and sum_n g q A
-    alignas(16) float dbc[kWarps][TT][2][N];
-    double dd[TT][CB][2];                    // sums of dD and ddt_bias, of each preparer
+    static constexpr int WARPS = K::NT / 32;
+    float2 du[K::TT][K::CB];                        // delta, delta x
+    alignas(16) float dy[K::TT][K::CB];
+    alignas(16) float bc[2][K::TT][K::N];
+    alignas(16) float part[3][K::TT][K::CB][K::YL]; // partial sums of y, du and sum_n g q A
+    alignas(16) float dbc[WARPS][K::TT][2][K::N];
+    double dd[K::TT][K::CB][2];                     // sums of dD and ddt_bias, of each preparer
 };
 
-// Sums 8 values over the 32 / LPC lanes that differ in the lane's channel.  Each shuffle
-// halves the values that a lane still holds; it ends with kKept of them, from at() on.
-template <int LPC>
+// Sums a lane's V values (NP of dB, NP of dC) over the M lanes of a warp that differ in their
+// channel.  Each shuffle halves the values that a lane still holds; it ends with kKept of
+// them, from at() on.
+template <class K>
 struct ChannelSum {
-    static constexpr int M = 32 / LPC;
-    static constexpr int kKept = M >= 8 ? 1 : 8 / M;
-    static __device__ __forceinline__ int at(int lane) { return M >= 8 ? (lane / LPC) / (M / 8) : (lane / LPC) * kKept; }
-    static __device__ __forceinline__ void run(float (&v)[8], int lane) {
-        int nv = 8;
+    static constexpr int M = 32 / K::LPC, V = 2 * K::NP;
+    static constexpr int kKept = M >= V ? 1 : V / M;
+    static __device__ __forceinline__ int at(int lane) { return M >= V ? lane / K::LPC / (M >= V ? M / V : 1) : lane / K::LPC * kKept; }
+    static __device__ __forceinline__ void run(float (&v)[V], int lane) {
+        int nv = V;
 #pragma unroll
         for (int o = M / 2; o > 0; o /= 2) {
             if (nv > 1) {
                 nv /= 2;
-                const bool up = lane & (o * LPC);
+                const bool up = lane & (o * K::LPC);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < V / 2; ++i)
                     if (i < nv) {
                         const float keep = up ? v[i + nv] : v[i], send = up ? v[i] : v[i + nv];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * LPC);
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * K::LPC);
                     }
             } else {
-                v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * LPC);
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * K::LPC);
             }
         }
     }
 };
 
-template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, class K, bool VEC>
+__global__ void __launch_bounds__(K::NT, kBwdBlocks)
 bwd_kernel(const __grid_constant__ Params p) {
-    constexpr int N = 4 * LPC, TT = Place<LPC>::TT, E = Place<LPC>::E, YL = BwdSmem<LPC>::YL, SUBS = TT / kSub;
-    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + kThreads - 1) / kThreads;
+    constexpr int N = K::N, TT = K::TT, E = K::E, PP = K::PP, NP = K::NP, SUBS = TT / kSub;
+    constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + K::NT - 1) / K::NT;
     extern __shared__ __align__(16) char smem_raw[];
-    BwdSmem<LPC>& sm = *reinterpret_cast<BwdSmem<LPC>*>(smem_raw);
-    const Place<LPC> at(p);
+    BwdSmem<K>& sm = *reinterpret_cast<BwdSmem<K>*>(smem_raw);
+    const Place<K> at(p);
     const int n = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long s, e;
     if (!p.seq.bounds(n, s, e)) return;   // reported by the first sweep
     const long tokens = p.seq.tokens();
     const long hrow = ((long)n * p.C + at.c) * N + at.n0;
-    Pair A2[2], g[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-    load_decays<LPC>(p, at, A2);
-    if (p.dh_final && at.on) load_pairs<4>(p.dh_final + hrow, g);
+    Pair A2[PP], g[PP] = {};
+    load_decays<K>(p, at, A2);
+    if (p.dh_final && at.on) load_pairs(p.dh_final + hrow, g);
     float bias[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -487,7 +486,7 @@ bwd_kernel(const __grid_constant__ Params p) {
         sm.dd[at.gt][at.gi + i][0] = sm.dd[at.gt][at.gi + i][1] = 0.0;
     }
     // long sums: in fp32 over kSub tokens (dA) or kFlush tiles (dD, ddt_bias), then in fp64
-    double dA[4] = {0.0, 0.0, 0.0, 0.0};
+    double dA[NP] = {};
     float dD[E], dbias[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) dD[i] = dbias[i] = 0.f;
@@ -511,19 +510,19 @@ bwd_kernel(const __grid_constant__ Params p) {
         orr = load_group<VEC, T, E>(p.dout, o, at.count);
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * kThreads, r = q % QUADS;
+            const int q = tid + k * K::NT, r = q % QUADS;
             const long tb = min(t0 + r / (N / 4), e - 1);
             br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
                 static_cast<const T*>(q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
         }
     };
     // the stored state before the sub-chunk in hand, read one sub-chunk ahead
-    Pair next[2];
+    Pair next[PP];
     const float* stored = nullptr;
     if (s < e) {
         fetch(s + (e - s - 1) / TT * TT);
         stored = p.ckpt + (ckpt_slot(s, n, (e - s - 1) / kSub) * p.C + at.c) * N + at.n0;
-        load_pairs<4>(stored, next);
+        load_pairs(stored, next);
     }
     for (long t0 = s + (e - s - 1) / TT * TT; t0 >= s && s < e; t0 -= TT) {
         const bool live = t0 + at.gt < e && at.count > 0;
@@ -534,12 +533,12 @@ bwd_kernel(const __grid_constant__ Params p) {
             const bool in = live && i < at.count;
             const float delta = in ? softplus(to_f(dt.v[i]) + bias[i]) : 0.f;
             const float o = in ? to_f(dout.v[i]) : 0.f;
-            sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)] = make_float2(delta, in ? delta * to_f(x.v[i]) : 0.f);
+            sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)] = make_float2(delta, in ? delta * to_f(x.v[i]) : 0.f);
             sm.dy[at.gt][at.gi + i] = p.z && in ? o * silu(to_f(z.v[i])) : o;
         }
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * kThreads;
+            const int q = tid + k * K::NT;
             float v[4];
             widen(br[k], v);
             const bool in = t0 + q % QUADS / (N / 4) < e;
@@ -552,19 +551,20 @@ bwd_kernel(const __grid_constant__ Params p) {
 #pragma unroll 1
         for (int k = SUBS - 1; k >= 0; --k) {
             if (t0 + k * kSub >= e) continue;
-            Pair a[kSub][2], q[kSub][2], dAk[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-            Pair h[2] = {next[0], next[1]};
+            Pair a[kSub][PP], q[kSub][PP], dAk[PP] = {}, h[PP];
+#pragma unroll
+            for (int i = 0; i < PP; ++i) h[i] = next[i];
             if (t0 + k * kSub > s) {
                 stored -= (long)p.C * N;
-                load_pairs<4>(stored, next);
+                load_pairs(stored, next);
             }
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                const float2 du = sm.du[k * kSub + j][du_slot<LPC>(j, at.li)];
-                Pair b[2];
-                load_pairs<4>(&sm.bc[0][k * kSub + j][at.n0], b);
+                const float2 du = sm.du[k * kSub + j][du_slot<K>(j, at.li)];
+                Pair b[PP];
+                load_pairs(&sm.bc[0][k * kSub + j][at.n0], b);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < PP; ++i) {
                     a[j][i] = exp2_pair(mul2(pair(du.x, du.x), A2[i]));
                     q[j][i] = mul2(a[j][i], h[i]);
                     h[i] = fma2(pair(du.y, du.y), b[i], q[j][i]);
@@ -573,23 +573,23 @@ bwd_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int j0 = kSub - kBatch; j0 >= 0; j0 -= kBatch) {
                 float2 du[kBatch];
-                float dy[kBatch], sums[3][kBatch], dbc[kBatch][ChannelSum<LPC>::kKept];
-                Pair b[kBatch][2], c[kBatch][2];
+                float dy[kBatch], sums[3][kBatch], dbc[kBatch][ChannelSum<K>::kKept];
+                Pair b[kBatch][PP], c[kBatch][PP];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const int t = k * kSub + j0 + j;
-                    du[j] = sm.du[t][du_slot<LPC>(t, at.li)];
+                    du[j] = sm.du[t][du_slot<K>(t, at.li)];
                     dy[j] = sm.dy[t][at.li];
-                    load_pairs<4>(&sm.bc[0][t][at.n0], b[j]);
-                    load_pairs<4>(&sm.bc[1][t][at.n0], c[j]);
+                    load_pairs(&sm.bc[0][t][at.n0], b[j]);
+                    load_pairs(&sm.bc[1][t][at.n0], c[j]);
                 }
 #pragma unroll
                 for (int j = kBatch - 1; j >= 0; --j) {
                     const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y), dd = pair(dy[j], dy[j]);
                     Pair y, gb, gqa;
-                    float v[8];
+                    float v[2 * NP];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < PP; ++i) {
                         const Pair qq = q[j0 + j][i], ht = fma2(u, b[j][i], qq);
                         g[i] = fma2(c[j][i], dd, g[i]);
                         const Pair gq = mul2(g[i], qq);
@@ -598,7 +598,7 @@ bwd_kernel(const __grid_constant__ Params p) {
                         gqa = i ? fma2(gq, A2[i], gqa) : mul2(gq, A2[i]);
                         dAk[i] = fma2(gq, dl, dAk[i]);
                         unpair(mul2(g[i], u), v[2 * i], v[2 * i + 1]);
-                        unpair(mul2(ht, dd), v[4 + 2 * i], v[5 + 2 * i]);
+                        unpair(mul2(ht, dd), v[NP + 2 * i], v[NP + 2 * i + 1]);
                         g[i] = mul2(a[j0 + j][i], g[i]);
                     }
                     float lo, hi;
@@ -609,26 +609,24 @@ bwd_kernel(const __grid_constant__ Params p) {
                     unpair(gqa, lo, hi);
                     sums[2][j] = lo + hi;
 #pragma unroll
-                    for (int m = 0; m < 3; ++m)
+                    for (int m = 0; m < 3; ++m) sums[m][j] = set_sum<K>(sums[m][j]);
+                    ChannelSum<K>::run(v, lane);
 #pragma unroll
-                        for (int o = LPC / YL / 2; o > 0; o /= 2) sums[m][j] += __shfl_xor_sync(0xffffffffu, sums[m][j], o);
-                    ChannelSum<LPC>::run(v, lane);
-#pragma unroll
-                    for (int i = 0; i < ChannelSum<LPC>::kKept; ++i) dbc[j][i] = v[i];
+                    for (int i = 0; i < ChannelSum<K>::kKept; ++i) dbc[j][i] = v[i];
                 }
-                const int ys = y_slot<YL>(at.li), vi = ChannelSum<LPC>::at(lane);
+                const int ys = y_slot<K>(at.li), vi = ChannelSum<K>::at(lane);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const int t = k * kSub + j0 + j;
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) sm.part[m][t][ys][tid % LPC / (LPC / YL)] = sums[m][j];
+                    for (int m = 0; m < 3; ++m) sm.part[m][t][ys][set_of<K>(tid)] = sums[m][j];
 #pragma unroll
-                    for (int i = 0; i < ChannelSum<LPC>::kKept; ++i)
-                        sm.dbc[warp][t][(vi + i) >> 2][at.n0 + ((vi + i) & 3)] = dbc[j][i];
+                    for (int i = 0; i < ChannelSum<K>::kKept; ++i)
+                        sm.dbc[warp][t][(vi + i) / NP][at.n0 + (vi + i) % NP] = dbc[j][i];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < PP; ++i) {
                 float lo, hi;
                 unpair(dAk[i], lo, hi);
                 dA[2 * i] += (double)lo;
@@ -644,12 +642,12 @@ bwd_kernel(const __grid_constant__ Params p) {
                 float sum[3];
 #pragma unroll
                 for (int m = 0; m < 3; ++m) {
-                    const float* l = sm.part[m][at.gt][y_slot<YL>(at.gi + i)];
+                    const float* l = sm.part[m][at.gt][y_slot<K>(at.gi + i)];
                     sum[m] = l[0] + l[1];
-                    if (YL == 4) sum[m] += l[2] + l[3];
+                    if (K::YL == 4) sum[m] += l[2] + l[3];
                 }
                 const float xv = to_f(x.v[i]), dy = sm.dy[at.gt][at.gi + i];
-                const float delta = sm.du[at.gt][du_slot<LPC>(at.gt, at.gi + i)].x;
+                const float delta = sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)].x;
                 const float D = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
                 dx[i] = fmaf(sum[1], delta, D * dy);
                 ddt[i] = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e)) * sigmoid(to_f(dt.v[i]) + bias[i]);
@@ -667,11 +665,11 @@ bwd_kernel(const __grid_constant__ Params p) {
             flush();
             since = 0;
         }
-        for (int i = tid; i < TT * 2 * N / 4; i += kThreads) {
+        for (int i = tid; i < TT * 2 * N / 4; i += K::NT) {
             if (t0 + i / (2 * N / 4) >= e) continue;
             float4 v = reinterpret_cast<const float4*>(&sm.dbc[0][0][0][0])[i];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
+            for (int w = 1; w < BwdSmem<K>::WARPS; ++w) {
                 const float4 o = reinterpret_cast<const float4*>(&sm.dbc[w][0][0][0])[i];
                 v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
             }
@@ -681,9 +679,9 @@ bwd_kernel(const __grid_constant__ Params p) {
     flush();
     __syncthreads();
     if (!at.on) return;
-    if (p.dh0) store_pairs<4>(p.dh0 + hrow, g);
+    if (p.dh0) store_pairs(p.dh0 + hrow, g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p.part_a[hrow + i] = dA[i];
+    for (int i = 0; i < NP; ++i) p.part_a[hrow + i] = dA[i];
     if (at.n0 == 0) {
         double sum[2] = {0.0, 0.0};
         for (int t = 0; t < TT; ++t)
@@ -737,14 +735,12 @@ sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ 
 // One token: the state h [B, C, N] is read and written once, which bounds it.  A block takes
 // kStepSeqs sequences of its channels, all their loads in flight together.
 constexpr int kStepSeqs = 4;
-template <typename T, int LPC>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class K>
+__global__ void __launch_bounds__(K::NT)
 step_kernel(const __grid_constant__ Params p) {
-    constexpr int N = 4 * LPC;
-    const Place<LPC> at(p);
-    if (!at.on) return;   // with all the lanes of its channel
+    constexpr int N = K::N;
+    const Place<K> at(p);
     const int first = blockIdx.y * kStepSeqs, count = min(p.seq.N - first, kStepSeqs);
-    const unsigned lanes = __activemask();
     float h[kStepSeqs][4], b[kStepSeqs][4], c[kStepSeqs][4], x[kStepSeqs], dt[kStepSeqs], z[kStepSeqs];
 #pragma unroll
     for (int k = 0; k < kStepSeqs; ++k) {
@@ -756,8 +752,8 @@ step_kernel(const __grid_constant__ Params p) {
         dt[k] = to_f(static_cast<const T*>(p.dt)[o]);
         z[k] = to_f(static_cast<const T*>(p.z ? p.z : p.x)[o]);
     }
-    Pair A2[2];
-    load_decays<LPC>(p, at, A2);
+    Pair A2[K::PP];
+    load_decays<K>(p, at, A2);
     const float bias = p.dt_bias ? p.dt_bias[at.c] : 0.f, D = p.D ? p.D[at.c] : 0.f;
 #pragma unroll
     for (int k = 0; k < kStepSeqs; ++k) {
@@ -774,10 +770,10 @@ step_kernel(const __grid_constant__ Params p) {
             h[k][2 * i + 1] = hi;
             y = fmaf(lo, c[k][2 * i], fmaf(hi, c[k][2 * i + 1], y));
         }
-        store_v<4>(p.h_final + o * N + at.n0, h[k]);
+        if (at.on) store_v<4>(p.h_final + o * N + at.n0, h[k]);
 #pragma unroll
-        for (int w = 1; w < LPC; w *= 2) y += __shfl_xor_sync(lanes, y, w);
-        if (at.n0 == 0) {
+        for (int w = 1; w < K::LPC; w *= 2) y += __shfl_xor_sync(0xffffffffu, y, w);
+        if (at.on && at.n0 == 0) {
             y = fmaf(D, x[k], y);
             static_cast<T*>(p.out)[o] = from_f<T>(p.z ? y * silu(z[k]) : y);
         }
