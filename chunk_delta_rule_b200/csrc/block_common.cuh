@@ -139,12 +139,16 @@ __device__ __forceinline__ float dsilu(float v) {
 }
 
 // softplus(v) = log(1 + e), e = exp(v); above 20 it is v to fp32 precision, -inf gives 0.
-// Up to e = 1/2 as 2 atanh(s) with s = e / (2 + e) <= 1/5, by atanh's series up to s^11 (the
-// next term is 6e-10 of the sum), which keeps the relative precision of small results;
-// above, from the hardware's logarithm of 1 + e, whose absolute error of 2^-22 is 6e-7 of
-// results of at least 0.4.
+// The exponent v log2(e) is taken in two parts, since its rounding alone would be 3e-7 of e at
+// v = -7, where time steps of 1e-3 lie.  Up to e = 1/2 as 2 atanh(s) with s = e / (2 + e) <=
+// 1/5, by atanh's series up to s^11 (the next term is 6e-10 of the sum), which keeps the
+// relative precision of small results; above, from the hardware's logarithm of 1 + e, whose
+// absolute error of 2^-22 is 6e-7 of results of at least 0.4.
 __device__ __forceinline__ float softplus(float v) {
-    const float e = exp2_fast(kLog2e * v);
+    const float w = fmaxf(v, -126.f);   // below, e is 0 to every sum it enters, and -inf has no rest
+    const float t = kLog2e * w, rest = fmaf(w, kLog2e, -t);
+    float e = exp2_fast(t);
+    e = v < -100.f ? 0.f : fmaf(e, rest * 0.693147181f, e);
     const float s = e * rcp_fast(2.f + e), q = s * s;
     float r = fmaf(q, 1.f / 11.f, 1.f / 9.f);
     r = fmaf(q, r, 1.f / 7.f);

@@ -300,6 +300,9 @@ def test_scan_padding_tokens_leave_the_state():
     ro, rh, _ = scan_reference(short, [0, 12], backward=False)
     check("state", hf, rh, SCAN)
     check("out", out[0, :12], ro, SCAN)
+    before = {k: (t[:, :12].contiguous() if k in TOKEN_KEYS and t is not None else t) for k, t in v.items()}
+    ba, bk, _ = scan_args(before)
+    assert torch.equal(hf, cdr.selective_scan(*ba, **bk)[1])     # not a bit moves
     g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"])
     for k in ("dx", "ddt", "dBm"):
         assert bool((g[k][0, 12:] == 0).all()), k
