@@ -94,6 +94,8 @@ class _Call:
 def _tokens(x, cu_seqlens, name: str = "x"):
     """(leading shape, N, T, C) of a token tensor: N sequences of T tokens, or T packed."""
     _element(x, name)
+    if max(x.shape, default=0) > 0x7FFFFFFF:
+        raise ValueError(f"{name} must have dimensions below 2^31 (got {tuple(x.shape)})")
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError(f"{name} must be [B, T, C]")

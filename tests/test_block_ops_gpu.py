@@ -636,3 +636,118 @@ def test_comba_block_prompt_then_decode():
     # the norm of what the recurrence gave: 5e-3 of the recurrence, and its own rounding
     want = ref.gated_norm(torch.from_numpy(np.asarray(ro)), gate, gw)
     check("block", cat(y, y1), want, 2 * 5e-3 + HALF[BF])
+
+
+# ---------------------------------------------------------------- the caller's buffers, refusals
+
+def test_the_callers_outputs_states_and_workspaces():
+    C, B, T, N = 72, 2, 300, 16
+    c = dev(conv_inputs(B * T, B, C, 4, BF, 8, True, True))
+    x, lib = c["x"].view(B, T, C), cdr.library()
+    want, wf = cdr.short_conv(x, c["weight"], c["bias"], c["init"])
+    out, fin = torch.empty_like(x), torch.empty_like(c["init"])
+    o, f = cdr.short_conv(x, c["weight"], c["bias"], c["init"], out=out, final_state=fin)
+    assert o is out and f is fin and torch.equal(out, want) and torch.equal(fin, wf)
+    assert cdr.short_conv(x, c["weight"], return_state=False)[1] is None
+    ws = torch.empty(lib.comba_short_conv_bwd_workspace_size(B, T, C, 4, 0), dtype=torch.uint8, device="cuda")
+    g, g2 = (cdr.short_conv_bwd(x, c["weight"], x, c["bias"], workspace=w) for w in (None, ws))
+    assert all(torch.equal(g[k], g2[k]) for k in ("dx", "dweight", "dbias"))
+    with pytest.raises(cdr.CombaError) as err:
+        cdr.short_conv_bwd(x, c["weight"], x, c["bias"], workspace=ws[:16])
+    assert err.value.status == -1
+    a, kw, v = scan_args(dev(scan_inputs(B * T, B, C, 1, N, BF, 9, "Dbzh")), (B, T))
+    want, wh = cdr.selective_scan(*a, **kw)
+    out, hf = torch.empty_like(x), torch.empty_like(kw["h0"])
+    ws = torch.empty(lib.comba_selective_scan_fwd_workspace_size(B, T, C, 1, N, 0) + 64, dtype=torch.uint8, device="cuda")
+    o, h = cdr.selective_scan(*a, **kw, out=out, h_final=hf, workspace=ws)
+    assert o is out and h is hf and torch.equal(out, want) and torch.equal(hf, wh)
+    ws = torch.empty(lib.comba_selective_scan_bwd_workspace_size(B, T, C, 1, N, 0), dtype=torch.uint8, device="cuda")
+    g, g2 = (cdr.selective_scan_bwd(*a, v["dout"], **kw, workspace=w) for w in (None, ws))
+    assert all(torch.equal(g[k], g2[k]) for k in g)
+    out = torch.empty_like(x)
+    assert cdr.gated_norm(x, x, kw["D"], out=out) is out and torch.equal(out, cdr.gated_norm(x, x, kw["D"]))
+
+
+def test_what_a_kernel_cannot_take_is_refused():
+    x = torch.zeros(2, 6, 16, device="cuda")
+    w, b = torch.zeros(16, 4, device="cuda"), torch.zeros(2, 6, 1, 16, device="cuda")
+    A = torch.zeros(16, 16, device="cuda")
+    for call in (lambda: cdr.short_conv(x.transpose(0, 1), w), lambda: cdr.short_conv(x, w.t().contiguous().t()),
+                 lambda: cdr.short_conv(x, w, initial_state=torch.zeros(2, 2, 16, device="cuda")),
+                 lambda: cdr.short_conv(x, w, out=x[:, :5]), lambda: cdr.short_conv(x, w.cpu()),
+                 lambda: cdr.selective_scan(x[..., ::2], x[..., ::2], A[:8], b, b),
+                 lambda: cdr.selective_scan(x, x, A, b, b[..., :8].contiguous()),
+                 lambda: cdr.gated_norm(x, x.cpu(), A[0]), lambda: cdr.gated_norm(x[:, ::2], x[:, ::2], A[0]),
+                 lambda: cdr.residual_norm(x, x[:1], A[0])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cdr.short_conv(x, w.bfloat16()), lambda: cdr.selective_scan(x, x.bfloat16(), A, b, b),
+                 lambda: cdr.selective_scan(x, x, A, b.bfloat16(), b), lambda: cdr.gated_norm(x, x, A[0].bfloat16()),
+                 lambda: cdr.residual_norm(x, x.bfloat16(), A[0])):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: cdr.short_conv(x, torch.zeros(16, 5, device="cuda")), lambda: cdr.short_conv(x, w, out=x),
+                 lambda: cdr.selective_scan(x, x, A[:, :12].contiguous(), b[..., :12].contiguous(), b[..., :12].contiguous()),
+                 lambda: cdr.selective_scan(x, x, A, b.repeat(1, 1, 3, 1), b.repeat(1, 1, 3, 1)),
+                 lambda: cdr.gated_norm(x, x, A[0], out=x), lambda: cdr.gated_norm(x, x, A[0], eps=-1.0)):
+        with pytest.raises(cdr.CombaError) as err:
+            call()
+        assert err.value.status == -1
+    wide = torch.zeros(2, 8193, device="cuda")
+    with pytest.raises(cdr.CombaError) as err:
+        cdr.gated_norm(wide, wide, wide[0])
+    assert err.value.status == -2
+
+
+# ---------------------------------------------------------------- sizes past 32-bit offsets
+
+def test_conv_and_norm_past_two_to_the_31_elements():
+    T, C, tail = (1 << 20) + 37, 2056, 64          # 2.16e9 elements
+    x = torch.randn(1, T, C, device="cuda", dtype=BF)
+    w = torch.randn(C, 4, device="cuda") * 0.5
+    out, fin = cdr.short_conv(x, w)
+    assert torch.equal(fin[0], x[0, -3:])
+    part, _ = cdr.short_conv(x[:, -tail:].contiguous(), w, initial_state=x[:, -tail - 3:-tail].contiguous())
+    assert torch.equal(out[:, -tail:], part)
+    g = cdr.short_conv_bwd(x, w, out)
+    gp = cdr.short_conv_bwd(x[:, -tail:].contiguous(), w, out[:, -tail:].contiguous(),
+                            initial_state=x[:, -tail - 3:-tail].contiguous())
+    assert torch.equal(g["dx"][:, -tail:], gp["dx"])
+    assert bool(torch.isfinite(g["dweight"]).all())
+    del out, part, g, gp
+    wn = torch.rand(C, device="cuda") + 0.5
+    y = cdr.gated_norm(x, x, wn)
+    assert torch.equal(y[:, -tail:], cdr.gated_norm(x[:, -tail:].contiguous(), x[:, -tail:].contiguous(), wn))
+    b = cdr.gated_norm_bwd(x, x, wn, y)
+    bp = cdr.gated_norm_bwd(x[:, -tail:].contiguous(), x[:, -tail:].contiguous(), wn, y[:, -tail:].contiguous())
+    assert torch.equal(b["dx"][:, -tail:], bp["dx"]) and torch.equal(b["dgate"][:, -tail:], bp["dgate"])
+    del b, bp
+    o, h = cdr.residual_norm(x, y, wn, scale=wn)
+    op, hp = cdr.residual_norm(x[:, -tail:].contiguous(), y[:, -tail:].contiguous(), wn, scale=wn)
+    assert torch.equal(o[:, -tail:], op) and torch.equal(h[:, -tail:], hp)
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == 0
+
+
+def test_scan_past_two_to_the_31_elements():
+    T, C, N, tail = (1 << 20) + 48, 2056, 8, 96     # 2.16e9 elements, more in the states' table
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, device="cuda", dtype=BF, generator=g)
+    x, dt, Bm, Cm = rand(1, T, C), rand(1, T, C), rand(1, T, 1, N), rand(1, T, 1, N)
+    A = torch.randn(C, N, device="cuda", generator=g) * 0.2
+    bias = torch.full((C,), -4.0, device="cuda")
+    cut = lambda t, s: t[:, s].contiguous()
+    head, end = slice(0, T - tail), slice(T - tail, T)
+    out, h = cdr.selective_scan(x, dt, A, Bm, Cm, dt_bias=bias)
+    _, hm = cdr.selective_scan(*(cut(t, head) for t in (x, dt)), A, *(cut(t, head) for t in (Bm, Cm)), dt_bias=bias)
+    po, ph = cdr.selective_scan(*(cut(t, end) for t in (x, dt)), A, *(cut(t, end) for t in (Bm, Cm)), dt_bias=bias, h0=hm)
+    check("out", out[:, end], po, SCAN + HALF[BF])
+    check("h_final", h, ph, SCAN)
+    b = cdr.selective_scan_bwd(x, dt, A, Bm, Cm, out, dt_bias=bias)
+    bp = cdr.selective_scan_bwd(*(cut(t, end) for t in (x, dt)), A, *(cut(t, end) for t in (Bm, Cm)), cut(out, end),
+                                dt_bias=bias, h0=hm)
+    for k in ("dx", "ddt", "dBm", "dCm"):
+        check(k, b[k][:, end], bp[k], SCAN_BWD + 2 * HALF[BF])
+    assert all(bool(torch.isfinite(b[k]).all()) for k in ("dA_log", "ddt_bias"))
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == 0
