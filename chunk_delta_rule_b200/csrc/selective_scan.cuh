@@ -512,6 +512,11 @@ bwd_kernel(const __grid_constant__ Params p) {
         dr = load_group<VEC, T, E>(p.dt, o, at.count);
         zr = load_group<VEC, T, E>(p.z ? p.z : p.x, o, at.count);
         orr = load_group<VEC, T, E>(p.dout, o, at.count);
+        const long ahead = max(min(t0 + at.gt, e - 1) - 2 * TT, s) * p.C + at.gc;
+        prefetch_l2(static_cast<const T*>(p.x) + ahead);
+        prefetch_l2(static_cast<const T*>(p.dt) + ahead);
+        prefetch_l2(static_cast<const T*>(p.dout) + ahead);
+        if (p.z) prefetch_l2(static_cast<const T*>(p.z) + ahead);
 #pragma unroll
         for (int k = 0; k < QP; ++k) {
             const int q = tid + k * K::NT, r = q % QUADS;
@@ -561,6 +566,7 @@ bwd_kernel(const __grid_constant__ Params p) {
             if (t0 + k * kSub > s) {
                 stored -= (long)p.C * N;
                 load_pairs(stored, next);
+                prefetch_l2(t0 + k * kSub > s + 2 * kSub ? stored - 2l * p.C * N : stored);
             }
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
