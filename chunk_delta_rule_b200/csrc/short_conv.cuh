@@ -11,6 +11,8 @@
 
 #include <limits.h>
 
+#include <type_traits>
+
 #include "block_common.cuh"
 
 namespace comba {
@@ -163,27 +165,35 @@ fwd_kernel(const __grid_constant__ Params p, long tiles, long total) {
         };
 #pragma unroll
         for (int k = 0; k < R::GROUPS - 1; ++k) fetch(k * kAhead);
-        for (int k0 = 0; k0 <= last; k0 += kAhead) {
+        auto token = [&](int at) {
+            ring.get(at % R::ROWS, 0, h[W - 1]);
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = b[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) fma_v<V>(w[j], h[j], y);
+            if (SILU)
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
+            store_v<V>(op + at * C, y);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
+        };
+        // whole groups without a condition between their tokens: h then moves on by renaming
+        int k0 = 0;
+        for (; k0 + kAhead <= last + 1; k0 += kAhead) {
             fetch(k0 + R::ROWS - kAhead);
             ring.template wait<R::GROUPS - 1>();
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                if (k0 + k > last) break;
-                ring.get((k0 + k) % R::ROWS, 0, h[W - 1]);
-                float y[V];
+            for (int k = 0; k < kAhead; ++k) token(k0 + k);
+        }
+        if (k0 <= last) {
+            ring.template wait<0>();
 #pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = b[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) fma_v<V>(w[j], h[j], y);
-                if (SILU)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
-                store_v<V>(op + (k0 + k) * C, y);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
-            }
+            for (int k = 0; k < kAhead - 1; ++k)
+                if (k0 + k <= last) token(k0 + k);
         }
         ring.template wait<0>();
         t = stop;
@@ -286,14 +296,15 @@ bwd_kernel(const __grid_constant__ Params p, long total) {
         const unsigned C = p.C;
         const T *xp = xb + from * p.C, *dp = ob + from * p.C;
         T* gp = static_cast<T*>(p.dx) + from * p.C + c;
-        // adds a token's d to the open dx and closes that of the token W - 1 before it
-        auto close = [&](int at, const float (&d)[V]) {
+        // adds a token's d to the open dx and closes that of the token W - 1 before it; END: the
+        // token lies behind the tile, and the closed one may reach into the final state
+        auto close = [&](int at, const float (&d)[V], auto END) {
 #pragma unroll
             for (int i = 0; i < V; ++i) g[W - 1][i] = w[W - 1][i] * d[i];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) fma_v<V>(w[j], d, g[j]);
             if (at >= W - 1) {
-                if (p.dfin && at >= rest) {
+                if (decltype(END)::value && p.dfin && at >= rest) {
                     float f[V];
                     load_v<V>(static_cast<const T*>(p.dfin) + ((long)n * (W - 1) + (at - rest)) * p.C + c, f);
 #pragma unroll
@@ -321,22 +332,30 @@ bwd_kernel(const __grid_constant__ Params p, long total) {
         };
 #pragma unroll
         for (int k = 0; k < R::GROUPS - 1; ++k) fetch(k * kAhead);
-        for (int k0 = 0; k0 < count; k0 += kAhead) {
+        auto token = [&](int at) {
+            float d[V];
+            ring.get(at % R::ROWS, 0, h[W - 1]);
+            ring.get(at % R::ROWS, 1, d);
+            dpre_of<W, V, SILU>(w, b, h, d);
+#pragma unroll
+            for (int i = 0; i < V; ++i) db[i] += d[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) fma_v<V>(d, h[j], dw[j]);
+            close(at, d, std::false_type());
+        };
+        // whole groups without a condition between their tokens: h and g then move on by renaming
+        int k0 = 0;
+        for (; k0 + kAhead <= count; k0 += kAhead) {
             fetch(k0 + R::ROWS - kAhead);
             ring.template wait<R::GROUPS - 1>();
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                if (k0 + k >= count) break;
-                float d[V];
-                ring.get((k0 + k) % R::ROWS, 0, h[W - 1]);
-                ring.get((k0 + k) % R::ROWS, 1, d);
-                dpre_of<W, V, SILU>(w, b, h, d);
+            for (int k = 0; k < kAhead; ++k) token(k0 + k);
+        }
+        if (k0 < count) {
+            ring.template wait<0>();
 #pragma unroll
-                for (int i = 0; i < V; ++i) db[i] += d[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) fma_v<V>(d, h[j], dw[j]);
-                close(k0 + k, d);
-            }
+            for (int k = 0; k < kAhead - 1; ++k)
+                if (k0 + k < count) token(k0 + k);
         }
         ring.template wait<0>();
         // the W-1 tokens behind the tile; past the sequence's end there is nothing to add
@@ -350,7 +369,7 @@ bwd_kernel(const __grid_constant__ Params p, long total) {
                 load_v<V>(dp + (count + k) * C, d);
                 dpre_of<W, V, SILU>(w, b, h, d);
             }
-            close(count + k, d);
+            close(count + k, d, std::true_type());
         }
         t = stop;
     }
