@@ -217,7 +217,6 @@ bool scan_vector(int C, int G, int dtype, std::initializer_list<const void*> ptr
 // Channel blocks of one group.
 int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, 4 * scan::Layout<16>::NT / N); }
 
-
 struct ScanWs {
     size_t ckpt, bc, a, d, total;   // byte offsets
 };
@@ -235,9 +234,11 @@ ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
 }
 
 // Pieces of the split form, 1 for the direct one.  Costs in clocks of an SM for 16 tokens of
-// a channel block, measured on B8 and B1 T4096..64K C2048 N16: 2950 where a block has its SM to
-// itself (latency), 1290 where 4 share it, and 700 for the split form's first sweep.  A packed
-// batch's longest sequence is taken to be 4 times the mean.
+// a channel block: 2950 where a block has its SM to itself (latency), 1290 where 4 share it, and
+// 700 for the split form's first sweep.  A packed batch's longest sequence is taken to be 4
+// times the mean.  Measured, direct and split: T4096 C2048 N16 of 1 sequence 328 and 130 us, of
+// 2 329 and 241, of 3 382 and 350, of 4 383 and 459; T16384 C64 1286 and 44; T512 C2048 46 and
+// 34; T300 C256 29 and 33.
 int scan_pieces(const Seqs& q, int C, int G, int N) {
     const double sm_blocks = (double)G * group_blocks(C, G, N) / kSMs;
     const double tiles = q.tokens() / 16.0, mean = tiles / q.N;

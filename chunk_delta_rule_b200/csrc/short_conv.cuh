@@ -6,7 +6,10 @@
 // with the W-1 inputs before a sequence's first token taken from its carried state.  Every
 // token is read and written once, so the kernels are bound by HBM bandwidth: a thread
 // keeps the filter and the last W-1 inputs of 4 neighbouring channels in registers and
-// walks a tile of tokens.
+// walks a tile of tokens (8 channels would take twice the registers, and halve the threads).
+// Measured on B8 T4096 C6144 W4 bf16: forward 133 us, 6.05 TB/s of a copy's 6.55; backward
+// 249 us, 4.85 TB/s, where the issue slots bound it (64 % busy with 16 warps an SM, which
+// the 72 values a thread keeps for its 4 channels' filter, sums and open rows allow).
 #pragma once
 
 #include <limits.h>
@@ -447,7 +450,9 @@ step_kernel(const T* __restrict__ x, const float* __restrict__ weight, const flo
 inline int step_sequences(long B, int cv) { return B * cv >= (long)kSMs * 512 * kStepSeqs ? kStepSeqs : 1; }
 
 // Tokens in a tile: long tiles read fewer tokens twice (W-1 a tile) and, in the backward,
-// write fewer partial sums; short ones give enough threads when the tokens are few.
+// write fewer partial sums; short ones give enough threads when the tokens are few.  On B8
+// T4096 C6144 tiles of up to 32, 64, 128 tokens took 137, 133, 135 us forward, and of up to 64,
+// 128, 256 tokens 265, 249, 251 us backward.
 inline int tile_tokens(long tokens, int cv, int most) {
     int L = most;
     while (L > 4 && ceil_div(tokens, L) * cv < (long)kSMs * 1024) L /= 2;
