@@ -52,22 +52,35 @@ def _device(t, name: str) -> int:
 
 
 class _Call:
-    """One call of the library: the device (of its first tensor), the stream, and the
-    buffers that are allocated here, which are kept for the caller's stream."""
-    __slots__ = ("first", "index", "stream", "made")
+    """One call of the library on the device of its first tensor.  Buffers that are
+    allocated here for a stream other than the current one come from that stream's memory,
+    which nothing on the current one may still be using, and are known to the current
+    stream, which is likely to read them."""
+    __slots__ = ("first", "index", "stream")
 
     def __init__(self, first, index: int, stream):
-        self.first, self.index, self.stream, self.made = first, index, stream, []
+        self.first, self.index, self.stream = first, index, None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            if stream.cuda_stream != torch.cuda.current_stream(index).cuda_stream:
+                self.stream = stream
+
+    def _alloc(self, make):
+        if self.stream is None:
+            return make()
+        with torch.cuda.stream(self.stream):
+            t = make()
+        t.record_stream(torch.cuda.current_stream(self.index))
+        return t
 
     def new(self, shape, dtype):
-        t = self.first.new_empty(shape, dtype=dtype)
-        self.made.append(t)
-        return t
+        return self._alloc(lambda: self.first.new_empty(shape, dtype=dtype))
 
     def like(self, t):
-        t = torch.empty_like(t)   # of a contiguous tensor: the quickest allocation
-        self.made.append(t)
-        return t
+        if self.stream is None:
+            return torch.empty_like(t)   # of a contiguous tensor: the quickest allocation
+        return self._alloc(lambda: torch.empty_like(t))
 
     def workspace(self, nbytes: int, given: Optional[torch.Tensor]):
         if given is None:
@@ -79,14 +92,12 @@ class _Call:
     def __call__(self, name: str, *args) -> None:
         fn = getattr(_cdr.library(), name)
         args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-        if torch.cuda.current_device() == self.index and self.stream is None:
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(self.index))
+        handle = torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None else self.stream.cuda_stream
+        if torch.cuda.current_device() == self.index:
+            st = fn(*args, handle)
         else:
-            device = torch.device("cuda", self.index)
-            with torch.cuda.device(device):
-                st = fn(*args, _cdr._stream_handle(device, self.stream))
-                for t in self.made:
-                    _cdr._keep_for_stream(t, device, self.stream)
+            with torch.cuda.device(self.index):
+                st = fn(*args, handle)
         if st != 0:
             raise _cdr.CombaError(st, name)
 

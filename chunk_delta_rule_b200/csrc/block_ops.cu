@@ -142,6 +142,7 @@ extern "C" int comba_short_conv_bwd(const void* x, const float* weight, const fl
                                     int dtype, void* workspace, size_t workspace_bytes, comba_stream_t stream) {
     if (N < 0 || T < 0 || C < 0 || W < 2 || W > 4 || !dtype_ok(dtype)) return COMBA_EINVAL;
     if (C == 0) return COMBA_OK;
+    if (N == 0) T = 0;   // no sequence covers a token
     if (C > conv::kMaxChannels) return COMBA_EUNSUPPORTED;
     const size_t e = elt_size(dtype), tokens = token_count(cu_seqlens, N, T);
     if (volume(tokens, C) > kMaxElements || volume(N, W - 1, C) > kMaxElements) return COMBA_EINVAL;
@@ -217,40 +218,37 @@ bool scan_vector(int C, int G, int dtype, std::initializer_list<const void*> ptr
 // Channel blocks of one group.
 int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, 4 * scan::Layout<16>::NT / N); }
 
-struct ScanWs {
-    size_t ckpt, bc, a, d, total;   // byte offsets
+// Pieces of the split form, 1 for the direct one, from the clocks that 16 tokens of a channel
+// block cost.  A packed batch's longest sequence is taken to be 4 times the mean.  Measured at
+// C2048 N16, direct and split, forward: T4096 of 1 sequence 328 and 130 us, of 2 329 and 241, of 3
+// 382 and 350, of 4 383 and 459; T512 46 and 34; T16384 C64 1286 and 44; T300 C256 29 and 33.
+// Backward: T4096 of 1 1030 and 557, of 2 1038 and 1073, of 3 1291 and 1565; T512 145 and 98;
+// T4096 C256 997 and 98.
+struct SplitCosts {
+    double lone, shared, more;   // clocks: alone on an SM, in a full one, the split form's sweeps
+    int blocks;                  // that an SM holds
 };
-
-ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
-    ScanWs w{};
-    size_t o = 0;
-    auto take = [&](size_t n) { const size_t at = o; o += (n + 255) & ~(size_t)255; return at; };
-    w.ckpt = take((size_t)scan::ckpt_slots(q) * C * N * 4);
-    w.bc = take((size_t)G * group_blocks(C, G, N) * q.tokens() * 2 * N * 4);
-    w.a = take((size_t)q.N * C * N * 8);
-    w.d = take((size_t)q.N * 2 * C * 8);
-    w.total = o;
-    return w;
-}
-
-// Pieces of the split form, 1 for the direct one.  Costs in clocks of an SM for 16 tokens of
-// a channel block: 2950 where a block has its SM to itself (latency), 1290 where 4 share it, and
-// 700 for the split form's first sweep.  A packed batch's longest sequence is taken to be 4
-// times the mean.  Measured, direct and split: T4096 C2048 N16 of 1 sequence 328 and 130 us, of
-// 2 329 and 241, of 3 382 and 350, of 4 383 and 459; T16384 C64 1286 and 44; T512 C2048 46 and
-// 34; T300 C256 29 and 33.
-int scan_pieces(const Seqs& q, int C, int G, int N) {
+constexpr SplitCosts kFwdCosts{2950, 1290, 700, 4}, kBwdCosts{7600, 4700, 1500, 2};
+int scan_pieces(const Seqs& q, int C, int G, int N, const SplitCosts& k) {
+    if (q.tokens() <= 0) return 1;
     const double sm_blocks = (double)G * group_blocks(C, G, N) / kSMs;
     const double tiles = q.tokens() / 16.0, mean = tiles / q.N;
     const double longest = q.cu ? (4 * mean < tiles ? 4 * mean : tiles) : mean;
-    const double direct = std::max(longest * 2950, tiles * sm_blocks * 1290), split = tiles * sm_blocks * (1290 + 700);
+    const double direct = std::max(longest * k.lone, tiles * sm_blocks * k.shared), split = tiles * sm_blocks * (k.shared + k.more);
     const long most = std::min<long>(128, q.tokens() / 128);
-    const long fit = (long)(4 / sm_blocks);      // one wave of 4 blocks an SM
+    const long fit = (long)(k.blocks / sm_blocks);   // one wave of blocks
     const long pieces = std::min(most, fit);
     return pieces >= 2 && split * std::max(1.0, fit / (double)pieces) < direct ? (int)pieces : 1;
 }
 
-// The split form's cut and workspace; `pieces` may come out smaller for the rounding.
+// Pieces of whole tiles; they may come out fewer than wanted.
+void cut(const Seqs& q, int want, long& piece, int& pieces) {
+    if (want < 2) return;
+    piece = ceil_div(ceil_div(q.tokens(), want), 32) * 32;
+    pieces = (int)ceil_div(q.tokens(), piece);
+}
+
+// The forward's cut and workspace (byte offsets).
 struct SplitWs {
     long piece = 0;
     int pieces = 1;
@@ -258,15 +256,39 @@ struct SplitWs {
 };
 SplitWs split_ws(const Seqs& q, int C, int G, int N) {
     SplitWs w;
-    const int want = q.tokens() > 0 ? scan_pieces(q, C, G, N) : 1;
-    if (want < 2) return w;
-    w.piece = ceil_div(ceil_div(q.tokens(), want), 32) * 32;
-    w.pieces = (int)ceil_div(q.tokens(), w.piece);
+    cut(q, scan_pieces(q, C, G, N, kFwdCosts), w.piece, w.pieces);
+    if (w.pieces < 2) return w;
     size_t o = 0;
     auto take = [&](size_t n) { const size_t at = o; o += (n + 255) & ~(size_t)255; return at; };
     w.ends = take((size_t)w.pieces * C * N * 4);
     w.dsum = take((size_t)w.pieces * C * 4);
     w.h0 = take((size_t)q.N * C * N * 4);
+    w.total = o;
+    return w;
+}
+
+// The backward's.
+struct ScanWs {
+    long piece = 0;
+    int pieces = 1;
+    size_t ckpt, bc, a, d, ends, back_ends, dsum, total;
+};
+
+ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
+    ScanWs w{};
+    size_t o = 0;
+    auto take = [&](size_t n) { const size_t at = o; o += (n + 255) & ~(size_t)255; return at; };
+    cut(q, scan_pieces(q, C, G, N, kBwdCosts), w.piece, w.pieces);
+    const size_t rows = w.pieces > 1 ? w.pieces : q.N;
+    w.ckpt = take((size_t)scan::ckpt_slots(q, w.pieces) * C * N * 4);
+    w.bc = take((size_t)G * group_blocks(C, G, N) * q.tokens() * 2 * N * 4);
+    w.a = take(rows * C * N * 8);
+    w.d = take(rows * 2 * C * 8);
+    if (w.pieces > 1) {
+        w.ends = take((size_t)w.pieces * C * N * 4);
+        w.back_ends = take((size_t)w.pieces * C * N * 4);
+        w.dsum = take((size_t)w.pieces * C * 4);
+    }
     w.total = o;
     return w;
 }
@@ -278,10 +300,10 @@ int scan_fwd(const scan::Params& p, cudaStream_t s) {
         const dim3 grid(bx, (unsigned)p.pieces);
         if (p.vec) {
             scan::ends_kernel<T, K, true><<<grid, K::NT, 0, s>>>(p);
-            scan::split_kernel<T, K, true><<<grid, K::NT, 0, s>>>(p);
+            scan::split_kernel<T, K, scan::kOutputs, true><<<grid, K::NT, 0, s>>>(p);
         } else {
             scan::ends_kernel<T, K, false><<<grid, K::NT, 0, s>>>(p);
-            scan::split_kernel<T, K, false><<<grid, K::NT, 0, s>>>(p);
+            scan::split_kernel<T, K, scan::kOutputs, false><<<grid, K::NT, 0, s>>>(p);
         }
         return launched();
     }
@@ -291,22 +313,26 @@ int scan_fwd(const scan::Params& p, cudaStream_t s) {
     return launched();
 }
 
+template <typename T, class K, bool VEC>
+int scan_bwd_vec(const scan::Params& p, cudaStream_t s) {
+    const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)(p.pieces > 1 ? p.pieces : p.seq.N));
+    constexpr int smem = (int)sizeof(scan::BwdSmem<K>);
+    const auto kernel = p.pieces > 1 ? scan::bwd_kernel<T, K, VEC, true> : scan::bwd_kernel<T, K, VEC, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return COMBA_ECUDA;
+    if (p.pieces > 1) {
+        scan::ends_kernel<T, K, VEC><<<grid, K::NT, 0, s>>>(p);
+        scan::split_kernel<T, K, scan::kStates, VEC><<<grid, K::NT, 0, s>>>(p);
+        scan::back_ends_kernel<T, K, VEC><<<grid, K::NT, 0, s>>>(p);
+    } else {
+        scan::fwd_kernel<T, K, scan::kStates, VEC><<<grid, K::NT, 0, s>>>(p);
+    }
+    kernel<<<grid, K::NT, smem, s>>>(p);
+    return launched();
+}
+
 template <typename T, class K>
 int scan_bwd(const scan::Params& p, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.G * group_blocks(p.C, p.G, p.N)), (unsigned)p.seq.N);
-    if (p.vec) scan::fwd_kernel<T, K, scan::kStates, true><<<grid, K::NT, 0, s>>>(p);
-    else scan::fwd_kernel<T, K, scan::kStates, false><<<grid, K::NT, 0, s>>>(p);
-    constexpr int smem = (int)sizeof(scan::BwdSmem<K>);
-    if (p.vec) {
-        if (cudaFuncSetAttribute(scan::bwd_kernel<T, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return COMBA_ECUDA;
-        scan::bwd_kernel<T, K, true><<<grid, K::NT, smem, s>>>(p);
-    } else {
-        if (cudaFuncSetAttribute(scan::bwd_kernel<T, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return COMBA_ECUDA;
-        scan::bwd_kernel<T, K, false><<<grid, K::NT, smem, s>>>(p);
-    }
-    return launched();
+    return p.vec ? scan_bwd_vec<T, K, true>(p, s) : scan_bwd_vec<T, K, false>(p, s);
 }
 
 template <typename T, class K>
@@ -324,7 +350,7 @@ int scan_sums(const scan::Params& p, void* dB, void* dC, float* dA_log, float* d
                                                                             p.seq, p.G, p.N, group_blocks(p.C, p.G, p.N));
     const long np = (long)p.C * p.N + 2 * p.C;
     scan::sum_params_kernel<<<(unsigned)ceil_div(np, 256), 256, 0, s>>>(p.part_a, p.part_d, p.A_log, dA_log, dD, dbias, p.seq,
-                                                                        p.C, p.N);
+                                                                        p.pieces, p.C, p.N);
     return launched();
 }
 
@@ -410,6 +436,7 @@ extern "C" int comba_selective_scan_bwd(const void* x, const void* dt, const flo
     const size_t tokens = nseq > 0 && T > 0 ? token_count(cu_seqlens, nseq, T) : 0;
     if (int st = scan_sizes(nseq, T, C, G, N, dtype, tokens)) return st;
     if (C == 0) return COMBA_OK;
+    if (nseq == 0) T = 0;   // no sequence covers a token
     if (!z != !dz) return COMBA_EINVAL;
     const size_t e = elt_size(dtype), nx = tokens * C * e, nb = tokens * G * N * e, ns = (size_t)nseq * C * N * 4;
     const size_t na = (size_t)C * N * 4, nc = (size_t)C * 4;
@@ -434,6 +461,13 @@ extern "C" int comba_selective_scan_bwd(const void* x, const void* dt, const flo
     p.part_bc = reinterpret_cast<float*>(w + ws.bc);
     p.part_a = reinterpret_cast<double*>(w + ws.a);
     p.part_d = reinterpret_cast<double*>(w + ws.d);
+    p.piece = ws.piece;
+    p.pieces = ws.pieces;
+    if (ws.pieces > 1) {
+        p.ends = reinterpret_cast<float*>(w + ws.ends);
+        p.back_ends = reinterpret_cast<float*>(w + ws.back_ends);
+        p.dsum = reinterpret_cast<float*>(w + ws.dsum);
+    }
     p.status = comba::status_word();
     if (!p.status) return COMBA_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -28,10 +28,11 @@ struct Params {
     int pieces;
     float* ends;                 // [pieces, C, N]: state after a piece (see ends_kernel)
     float* dsum;                 // [pieces, C]: sum of delta over it
+    float* back_ends;            // [pieces, C, N]: gradient of the state before a piece (see back_ends_kernel)
     float* ckpt;                 // [slots, C, N]: the state before every kSub-th token of a sequence
     float* part_bc;              // [channel blocks, tokens, 2, N]
-    double* part_a;              // [sequences, C, N]
-    double* part_d;              // [sequences, 2, C]: dD and ddt_bias
+    double* part_a;              // [sequences or pieces, C, N]
+    double* part_d;              // [sequences or pieces, 2, C]: dD and ddt_bias
     Seqs seq;
     int C, G, N;
     bool vec;                    // groups of channels lie whole and aligned (see load_group)
@@ -57,11 +58,11 @@ __device__ __forceinline__ void store_pairs(float* p, const Pair (&v)[2]) {
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
 }
 
-// Slot of the stored state of sub-chunk k of sequence n that starts at token s: a sequence
-// of l tokens has ceil(l / kSub) of them, and s / kSub + n leaves room for them before the
-// next sequence's.
+// Slot of the stored state of sub-chunk k of the n-th run of tokens (a sequence, or its part in
+// a piece) that starts at token s: a run of l tokens has ceil(l / kSub) of them, and
+// s / kSub + n leaves room for them before the next run's.
 __host__ __device__ inline long ckpt_slot(long s, int n, long k) { return s / kSub + n + k; }
-inline long ckpt_slots(const Seqs& q) { return q.tokens() / kSub + q.N + 1; }
+inline long ckpt_slots(const Seqs& q, int pieces) { return q.tokens() / kSub + q.N + pieces + 1; }
 
 // How the kernels lay out N state entries: NP a lane, LPC lanes a channel, NT threads a block
 // (CB channels), and tiles of TT tokens, which a block stages in shared memory at a time.
@@ -178,7 +179,7 @@ enum Mode {
     kEnds       // no outputs, only the state after the last token (the split form's first sweep)
 };
 
-// Tokens [from, to) of sequence n, which starts at token s, from and to the state h of the
+// Tokens [from, to), the n-th run of tokens (see ckpt_slot), from and to the state h of the
 // block's lanes, a tile at a time.
 //
 // A tile passes through three phases.  (1) Each (token, channel) has one thread, which forms
@@ -193,7 +194,7 @@ enum Mode {
 // issue slots 51 %; a block's own chain of phases leaves them idle, and the registers and the
 // 3.5 blocks an SM has do not fill the gaps.
 template <typename T, class K, Mode M, bool VEC>
-__device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Place<K>& at, int n, long s, long from,
+__device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Place<K>& at, int n, long from,
                                      long to, const Pair (&A2)[K::PP], Pair (&h)[K::PP], float& dsum) {
     constexpr int N = K::N, TT = K::TT, E = K::E, PP = K::PP;
     constexpr int QUADS = TT * N / 4, QP = (2 * QUADS + K::NT - 1) / K::NT;   // of B and C
@@ -277,7 +278,7 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Plac
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (M == kStates && (j0 + j) % kSub == 0 && at.on && t0 + j0 + j < to)
-                    store_pairs(p.ckpt + (ckpt_slot(s, n, (t0 - s + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
+                    store_pairs(p.ckpt + (ckpt_slot(from, n, (t0 - from + j0 + j) / kSub) * p.C + at.c) * N + at.n0, h);
                 Pair acc;
 #pragma unroll
                 for (int i = 0; i < PP; ++i) {
@@ -338,7 +339,7 @@ fwd_kernel(const __grid_constant__ Params p) {
     float dsum;
     load_decays<K>(p, at, A2);
     if (p.h0) load_pairs(p.h0 + hrow, h);
-    walk<T, K, M, VEC>(p, sm, at, n, s, s, e, A2, h, dsum);
+    walk<T, K, M, VEC>(p, sm, at, n, s, e, A2, h, dsum);
     if (M == kOutputs && p.h_final && at.on) store_pairs(p.h_final + hrow, h);
 }
 
@@ -361,7 +362,7 @@ ends_kernel(const __grid_constant__ Params p) {
     float dsum = 0.f;
     load_decays<K>(p, at, A2);
     if (s >= t0 && p.h0) load_pairs(p.h0 + ((long)n * p.C + at.c) * K::N + at.n0, h);
-    walk<T, K, kEnds, VEC>(p, sm, at, n, s, max(s, t0), t1, A2, h, dsum);
+    walk<T, K, kEnds, VEC>(p, sm, at, n, max(s, t0), t1, A2, h, dsum);
     if (!at.on) return;
     const long row = (long)blockIdx.y * p.C + at.c;
     store_pairs(p.ends + row * K::N + at.n0, h);
@@ -369,8 +370,8 @@ ends_kernel(const __grid_constant__ Params p) {
 }
 
 // Second sweep: every piece again, each sequence in it from its start state, which the
-// block composes from the pieces before it.
-template <typename T, class K, bool VEC>
+// block composes from the pieces before it.  (kStates: the same for the backward's first sweep.)
+template <typename T, class K, Mode M, bool VEC>
 __global__ void __launch_bounds__(K::NT)
 split_kernel(const __grid_constant__ Params p) {
     constexpr int N = K::N;
@@ -381,7 +382,7 @@ split_kernel(const __grid_constant__ Params p) {
         long s, e;
         const bool ok = p.seq.bounds(n, s, e);
         if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, COMBA_EINVAL);
-        if (!ok || s < e || !p.h_final || !at.on) continue;
+        if (!ok || s < e || M != kOutputs || !p.h_final || !at.on) continue;
         Pair h[K::PP] = {};
         const long hrow = ((long)n * p.C + at.c) * N + at.n0;
         if (p.h0) load_pairs(p.h0 + hrow, h);
@@ -414,8 +415,8 @@ split_kernel(const __grid_constant__ Params p) {
                 for (int k = 0; k < K::PP; ++k) h[k] = fma2(decay_pair(pair(ds, ds), A2[k]), h[k], r[k]);
             }
         }
-        walk<T, K, kOutputs, VEC>(p, sm, at, n, s, t, stop, A2, h, dsum);
-        if (stop == e && p.h_final && at.on) store_pairs(p.h_final + hrow, h);
+        walk<T, K, M, VEC>(p, sm, at, n + j, t, stop, A2, h, dsum);
+        if (M == kOutputs && stop == e && p.h_final && at.on) store_pairs(p.h_final + hrow, h);
         t = stop;
     }
 }
@@ -478,7 +479,90 @@ struct ChannelSum {
     }
 };
 
+// The backward's split form: a sequence's gradient of the state goes from g behind a piece to
+// exp(A sum delta) g + r before it.  For a piece that starts inside a sequence, r from that
+// sequence's tokens in it (from dh_final where the sequence ends there, so that r is the
+// gradient itself); sum delta is the forward's (ends_kernel).
 template <typename T, class K, bool VEC>
+__global__ void __launch_bounds__(K::NT)
+back_ends_kernel(const __grid_constant__ Params p) {
+    constexpr int N = K::N, TT = K::TT, E = K::E, PP = K::PP;
+    constexpr int QUADS = TT * N / 4, QP = (QUADS + K::NT - 1) / K::NT;   // of C
+    __shared__ FwdSmem<K> sm;   // du: delta and dy, bc[1]: C
+    const Place<K> at(p);
+    const long begin = blockIdx.y * p.piece;
+    const int n = p.seq.find(begin), tid = threadIdx.x;
+    long s, e;
+    if (!p.seq.bounds(n, s, e) || s >= begin || e <= begin) return;
+    const long to = min(e, begin + p.piece);
+    Pair A2[PP], g[PP] = {};
+    load_decays<K>(p, at, A2);
+    if (to == e && p.dh_final) load_pairs(p.dh_final + ((long)n * p.C + at.c) * N + at.n0, g);
+    float bias[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) bias[i] = p.dt_bias && i < at.count ? p.dt_bias[at.gc + i] : 0.f;
+    Group<T, E> dr, zr, orr;
+    typename Raw4<T>::type cr[QP];
+    auto fetch = [&](long t0) {
+        const long o = min(t0 + at.gt, to - 1) * p.C + at.gc;
+        dr = load_group<VEC, T, E>(p.dt, o, at.count);
+        zr = load_group<VEC, T, E>(p.z ? p.z : p.dout, o, at.count);
+        orr = load_group<VEC, T, E>(p.dout, o, at.count);
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = min(tid + k * K::NT, QUADS - 1);
+            const long tc = min(t0 + q / (N / 4), to - 1);
+            cr[k] = *reinterpret_cast<const typename Raw4<T>::type*>(static_cast<const T*>(p.Cm) + (tc * p.G + at.g) * N +
+                                                                     q % (N / 4) * 4);
+        }
+    };
+    long t0 = begin + (to - begin - 1) / TT * TT;
+    fetch(t0);
+    for (; t0 >= begin; t0 -= TT) {
+        const bool live = t0 + at.gt < to;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            // past the end: delta = 0 and dy = 0 leave g as it is
+            const float o = to_f(orr.v[i]), dy = p.z ? o * silu(to_f(zr.v[i])) : o;
+            sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)] =
+                live ? make_float2(softplus(to_f(dr.v[i]) + bias[i]), dy) : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int q = tid + k * K::NT;
+            float v[4];
+            widen(cr[k], v);
+            const bool in = t0 + q / (N / 4) < to;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
+            if (q < QUADS) store_v<4>(&sm.bc[1][0][0] + q * 4, v);
+        }
+        __syncthreads();
+        if (t0 > begin) fetch(t0 - TT);
+#pragma unroll
+        for (int j0 = TT - kBatch; j0 >= 0; j0 -= kBatch) {
+            Pair a[kBatch][PP], c[kBatch][PP];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const float2 dd = sm.du[j0 + j][du_slot<K>(j0 + j, at.li)];
+                load_pairs(&sm.bc[1][j0 + j][at.n0], c[j]);
+#pragma unroll
+                for (int i = 0; i < PP; ++i) {
+                    a[j][i] = decay_pair(pair(dd.x, dd.x), A2[i]);
+                    c[j][i] = mul2(pair(dd.y, dd.y), c[j][i]);
+                }
+            }
+#pragma unroll
+            for (int j = kBatch - 1; j >= 0; --j)
+#pragma unroll
+                for (int i = 0; i < PP; ++i) g[i] = fma2(a[j][i], g[i], mul2(a[j][i], c[j][i]));
+        }
+        __syncthreads();
+    }
+    if (at.on) store_pairs(p.back_ends + ((long)blockIdx.y * p.C + at.c) * N + at.n0, g);
+}
+
+template <typename T, class K, bool VEC, bool SPLIT>
 __global__ void __launch_bounds__(K::NT, kBwdBlocks)
 bwd_kernel(const __grid_constant__ Params p) {
     constexpr int N = K::N, TT = K::TT, E = K::E, PP = K::PP, NP = K::NP, SUBS = TT / kSub;
@@ -486,14 +570,10 @@ bwd_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) char smem_raw[];
     BwdSmem<K>& sm = *reinterpret_cast<BwdSmem<K>*>(smem_raw);
     const Place<K> at(p);
-    const int n = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long s, e;
-    if (!p.seq.bounds(n, s, e)) return;   // reported by the first sweep
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long tokens = p.seq.tokens();
-    const long hrow = ((long)n * p.C + at.c) * N + at.n0;
-    Pair A2[PP], g[PP] = {};
+    Pair A2[PP];
     load_decays<K>(p, at, A2);
-    if (p.dh_final && at.on) load_pairs(p.dh_final + hrow, g);
     float bias[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -514,202 +594,241 @@ bwd_kernel(const __grid_constant__ Params p) {
         }
     };
     int since = 0;
+    if (SPLIT && p.dh0)   // sequences without tokens
+        for (int n = row; n < p.seq.N; n += p.pieces) {
+            long s, e;
+            if (!p.seq.bounds(n, s, e) || s < e || !at.on) continue;
+            const long hrow = ((long)n * p.C + at.c) * N + at.n0;
+            Pair g[PP] = {};
+            if (p.dh_final) load_pairs(p.dh_final + hrow, g);
+            store_pairs(p.dh0 + hrow, g);
+        }
 
-    Group<T, E> xr, dr, zr, orr;
-    typename Raw4<T>::type br[QP];
-    auto fetch = [&](long t0) {
-        const long o = min(t0 + at.gt, e - 1) * p.C + at.gc;
-        xr = load_group<VEC, T, E>(p.x, o, at.count);
-        dr = load_group<VEC, T, E>(p.dt, o, at.count);
-        zr = load_group<VEC, T, E>(p.z ? p.z : p.x, o, at.count);
-        orr = load_group<VEC, T, E>(p.dout, o, at.count);
-        const long ahead = max(min(t0 + at.gt, e - 1) - 2 * TT, s) * p.C + at.gc;
-        prefetch_l2(static_cast<const T*>(p.x) + ahead);
-        prefetch_l2(static_cast<const T*>(p.dt) + ahead);
-        prefetch_l2(static_cast<const T*>(p.dout) + ahead);
-        if (p.z) prefetch_l2(static_cast<const T*>(p.z) + ahead);
-#pragma unroll
-        for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * K::NT, r = q % QUADS;
-            const long tb = min(t0 + r / (N / 4), e - 1);
-            br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
-                static_cast<const T*>(q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
+    // one sequence, or the piece's parts [s, e) of sequences, the last one first
+    const long begin = SPLIT ? row * p.piece : 0, end = SPLIT ? min(begin + p.piece, tokens) : tokens;
+    for (int n = SPLIT ? p.seq.find(end - 1) : row; n >= 0; --n) {
+        long first, last;   // of the whole sequence
+        const bool sound = p.seq.bounds(n, first, last);   // if not: reported by the first sweep
+        if (SPLIT && sound && last <= begin) break;
+        const long s = SPLIT ? max(first, begin) : first, e = SPLIT ? min(last, end) : last;
+        if (!sound || (SPLIT && s >= e)) {
+            if (SPLIT) continue;
+            return;
         }
-    };
-    // the stored state before the sub-chunk in hand, read one sub-chunk ahead
-    Pair next[PP];
-    const float* stored = nullptr;
-    if (s < e) {
-        fetch(s + (e - s - 1) / TT * TT);
-        stored = p.ckpt + (ckpt_slot(s, n, (e - s - 1) / kSub) * p.C + at.c) * N + at.n0;
-        load_pairs(stored, next);
-    }
-    for (long t0 = s + (e - s - 1) / TT * TT; t0 >= s && s < e; t0 -= TT) {
-        const bool live = t0 + at.gt < e && at.count > 0;
-        const Group<T, E> x = xr, dt = dr, z = zr, dout = orr;
+        const long hrow = ((long)n * p.C + at.c) * N + at.n0;
+        Pair g[PP] = {};
+        if (e == last) {
+            if (p.dh_final && at.on) load_pairs(p.dh_final + hrow, g);
+        } else {   // composed from the pieces behind this one
+            const int ends_in = (int)((last - 1) / p.piece);
+            load_pairs(p.back_ends + ((long)ends_in * p.C + at.c) * N + at.n0, g);
+#pragma unroll 4
+            for (int i = ends_in - 1; i > row; --i) {
+                const long q = (long)i * p.C + at.c;
+                const float ds = p.dsum[q];
+                Pair r[PP];
+                load_pairs(p.back_ends + q * N + at.n0, r);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            // past the end, and for channels that do not exist: nothing reaches g or a sum
-            const bool in = live && i < at.count;
-            const float delta = in ? softplus(to_f(dt.v[i]) + bias[i]) : 0.f;
-            const float o = in ? to_f(dout.v[i]) : 0.f;
-            sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)] = make_float2(delta, in ? delta * to_f(x.v[i]) : 0.f);
-            sm.dy[at.gt][at.gi + i] = p.z && in ? o * silu(to_f(z.v[i])) : o;
-        }
-#pragma unroll
-        for (int k = 0; k < QP; ++k) {
-            const int q = tid + k * K::NT;
-            float v[4];
-            widen(br[k], v);
-            const bool in = t0 + q % QUADS / (N / 4) < e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
-            if (q < 2 * QUADS) store_v<4>(&sm.bc[0][0][0] + q * 4, v);
-        }
-        __syncthreads();
-        if (t0 > s) fetch(t0 - TT);
-#pragma unroll 1
-        for (int k = SUBS - 1; k >= 0; --k) {
-            if (t0 + k * kSub >= e) continue;
-            Pair a[kSub][PP], q[kSub][PP], dAk[PP] = {}, h[PP];
-#pragma unroll
-            for (int i = 0; i < PP; ++i) h[i] = next[i];
-            if (t0 + k * kSub > s) {
-                stored -= (long)p.C * N;
-                load_pairs(stored, next);
-                prefetch_l2(t0 + k * kSub > s + 2 * kSub ? stored - 2l * p.C * N : stored);
-            }
-#pragma unroll
-            for (int j = 0; j < kSub; ++j) {
-                const float2 du = sm.du[k * kSub + j][du_slot<K>(j, at.li)];
-                Pair b[PP];
-                load_pairs(&sm.bc[0][k * kSub + j][at.n0], b);
-#pragma unroll
-                for (int i = 0; i < PP; ++i) {
-                    a[j][i] = decay_pair(pair(du.x, du.x), A2[i]);
-                    q[j][i] = mul2(a[j][i], h[i]);
-                    h[i] = fma2(pair(du.y, du.y), b[i], q[j][i]);
-                }
-            }
-#pragma unroll
-            for (int j0 = kSub - kBatch; j0 >= 0; j0 -= kBatch) {
-                float2 du[kBatch];
-                float dy[kBatch], sums[3][kBatch], dbc[kBatch][ChannelSum<K>::kKept];
-                Pair b[kBatch][PP], c[kBatch][PP];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int t = k * kSub + j0 + j;
-                    du[j] = sm.du[t][du_slot<K>(t, at.li)];
-                    dy[j] = sm.dy[t][at.li];
-                    load_pairs(&sm.bc[0][t][at.n0], b[j]);
-                    load_pairs(&sm.bc[1][t][at.n0], c[j]);
-                }
-#pragma unroll
-                for (int j = kBatch - 1; j >= 0; --j) {
-                    const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y), dd = pair(dy[j], dy[j]);
-                    Pair y, gb, gqa;
-                    float v[2 * NP];
-#pragma unroll
-                    for (int i = 0; i < PP; ++i) {
-                        const Pair qq = q[j0 + j][i], ht = fma2(u, b[j][i], qq);
-                        g[i] = fma2(c[j][i], dd, g[i]);
-                        const Pair gq = mul2(g[i], qq);
-                        y = i ? fma2(ht, c[j][i], y) : mul2(ht, c[j][i]);
-                        gb = i ? fma2(g[i], b[j][i], gb) : mul2(g[i], b[j][i]);
-                        gqa = i ? fma2(gq, A2[i], gqa) : mul2(gq, A2[i]);
-                        dAk[i] = fma2(gq, dl, dAk[i]);
-                        unpair(mul2(g[i], u), v[2 * i], v[2 * i + 1]);
-                        unpair(mul2(ht, dd), v[NP + 2 * i], v[NP + 2 * i + 1]);
-                        g[i] = mul2(a[j0 + j][i], g[i]);
-                    }
-                    float lo, hi;
-                    unpair(y, lo, hi);
-                    sums[0][j] = lo + hi;
-                    unpair(gb, lo, hi);
-                    sums[1][j] = lo + hi;
-                    unpair(gqa, lo, hi);
-                    sums[2][j] = lo + hi;
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) sums[m][j] = set_sum<K>(sums[m][j]);
-                    ChannelSum<K>::run(v, lane);
-#pragma unroll
-                    for (int i = 0; i < ChannelSum<K>::kKept; ++i) dbc[j][i] = v[i];
-                }
-                const int ys = y_slot<K>(at.li), vi = ChannelSum<K>::at(lane);
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int t = k * kSub + j0 + j;
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) sm.part[m][t][ys][set_of<K>(tid)] = sums[m][j];
-#pragma unroll
-                    for (int i = 0; i < ChannelSum<K>::kKept; ++i)
-                        sm.dbc[warp][t][(vi + i) / NP][at.n0 + (vi + i) % NP] = dbc[j][i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < PP; ++i) {
-                float lo, hi;
-                unpair(dAk[i], lo, hi);
-                dA[2 * i] += (double)lo;
-                dA[2 * i + 1] += (double)hi;
+                for (int k = 0; k < PP; ++k) g[k] = fma2(decay_pair(pair(ds, ds), A2[k]), g[k], r[k]);
             }
         }
-        __syncthreads();
-        if (live) {
-            const long o = (t0 + at.gt) * p.C + at.gc;
-            float dx[E], ddt[E], dz[E];
+        Group<T, E> xr, dr, zr, orr;
+        typename Raw4<T>::type br[QP];
+        auto fetch = [&](long t0) {
+            const long o = min(t0 + at.gt, e - 1) * p.C + at.gc;
+            xr = load_group<VEC, T, E>(p.x, o, at.count);
+            dr = load_group<VEC, T, E>(p.dt, o, at.count);
+            zr = load_group<VEC, T, E>(p.z ? p.z : p.x, o, at.count);
+            orr = load_group<VEC, T, E>(p.dout, o, at.count);
+            const long ahead = max(min(t0 + at.gt, e - 1) - 2 * TT, s) * p.C + at.gc;
+            prefetch_l2(static_cast<const T*>(p.x) + ahead);
+            prefetch_l2(static_cast<const T*>(p.dt) + ahead);
+            prefetch_l2(static_cast<const T*>(p.dout) + ahead);
+            if (p.z) prefetch_l2(static_cast<const T*>(p.z) + ahead);
+#pragma unroll
+            for (int k = 0; k < QP; ++k) {
+                const int q = tid + k * K::NT, r = q % QUADS;
+                const long tb = min(t0 + r / (N / 4), e - 1);
+                br[k] = *reinterpret_cast<const typename Raw4<T>::type*>(
+                    static_cast<const T*>(q >= QUADS ? p.Cm : p.Bm) + (tb * p.G + at.g) * N + r % (N / 4) * 4);
+            }
+        };
+        // the stored state before the sub-chunk in hand, read one sub-chunk ahead
+        Pair next[PP];
+        const float* stored = nullptr;
+        if (s < e) {
+            fetch(s + (e - s - 1) / TT * TT);
+            stored = p.ckpt + (ckpt_slot(s, SPLIT ? n + row : n, (e - s - 1) / kSub) * p.C + at.c) * N + at.n0;
+            load_pairs(stored, next);
+        }
+        for (long t0 = s + (e - s - 1) / TT * TT; t0 >= s && s < e; t0 -= TT) {
+            const bool live = t0 + at.gt < e && at.count > 0;
+            const Group<T, E> x = xr, dt = dr, z = zr, dout = orr;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                float sum[3];
+                // past the end, and for channels that do not exist: nothing reaches g or a sum
+                const bool in = live && i < at.count;
+                const float delta = in ? softplus(to_f(dt.v[i]) + bias[i]) : 0.f;
+                const float o = in ? to_f(dout.v[i]) : 0.f;
+                sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)] = make_float2(delta, in ? delta * to_f(x.v[i]) : 0.f);
+                sm.dy[at.gt][at.gi + i] = p.z && in ? o * silu(to_f(z.v[i])) : o;
+            }
 #pragma unroll
-                for (int m = 0; m < 3; ++m) {
-                    const float* l = sm.part[m][at.gt][y_slot<K>(at.gi + i)];
-                    sum[m] = l[0] + l[1];
-                    if (K::YL == 4) sum[m] += l[2] + l[3];
+            for (int k = 0; k < QP; ++k) {
+                const int q = tid + k * K::NT;
+                float v[4];
+                widen(br[k], v);
+                const bool in = t0 + q % QUADS / (N / 4) < e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = in ? v[i] : 0.f;
+                if (q < 2 * QUADS) store_v<4>(&sm.bc[0][0][0] + q * 4, v);
+            }
+            __syncthreads();
+            if (t0 > s) fetch(t0 - TT);
+#pragma unroll 1
+            for (int k = SUBS - 1; k >= 0; --k) {
+                if (t0 + k * kSub >= e) continue;
+                Pair a[kSub][PP], q[kSub][PP], dAk[PP] = {}, h[PP];
+#pragma unroll
+                for (int i = 0; i < PP; ++i) h[i] = next[i];
+                if (t0 + k * kSub > s) {
+                    stored -= (long)p.C * N;
+                    load_pairs(stored, next);
+                    prefetch_l2(t0 + k * kSub > s + 2 * kSub ? stored - 2l * p.C * N : stored);
                 }
-                const float xv = to_f(x.v[i]), dy = sm.dy[at.gt][at.gi + i];
-                const float delta = sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)].x;
-                const float D = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
-                dx[i] = fmaf(sum[1], delta, D * dy);
-                ddt[i] = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e)) * sigmoid(to_f(dt.v[i]) + bias[i]);
-                dz[i] = p.z ? to_f(dout.v[i]) * fmaf(D, xv, sum[0]) * dsilu(to_f(z.v[i])) : 0.f;
-                if (i < at.count) {
-                    dD[i] = fmaf(dy, xv, dD[i]);
-                    dbias[i] += ddt[i];
+#pragma unroll
+                for (int j = 0; j < kSub; ++j) {
+                    const float2 du = sm.du[k * kSub + j][du_slot<K>(j, at.li)];
+                    Pair b[PP];
+                    load_pairs(&sm.bc[0][k * kSub + j][at.n0], b);
+#pragma unroll
+                    for (int i = 0; i < PP; ++i) {
+                        a[j][i] = decay_pair(pair(du.x, du.x), A2[i]);
+                        q[j][i] = mul2(a[j][i], h[i]);
+                        h[i] = fma2(pair(du.y, du.y), b[i], q[j][i]);
+                    }
+                }
+#pragma unroll
+                for (int j0 = kSub - kBatch; j0 >= 0; j0 -= kBatch) {
+                    float2 du[kBatch];
+                    float dy[kBatch], sums[3][kBatch], dbc[kBatch][ChannelSum<K>::kKept];
+                    Pair b[kBatch][PP], c[kBatch][PP];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int t = k * kSub + j0 + j;
+                        du[j] = sm.du[t][du_slot<K>(t, at.li)];
+                        dy[j] = sm.dy[t][at.li];
+                        load_pairs(&sm.bc[0][t][at.n0], b[j]);
+                        load_pairs(&sm.bc[1][t][at.n0], c[j]);
+                    }
+#pragma unroll
+                    for (int j = kBatch - 1; j >= 0; --j) {
+                        const Pair dl = pair(du[j].x, du[j].x), u = pair(du[j].y, du[j].y), dd = pair(dy[j], dy[j]);
+                        Pair y, gb, gqa;
+                        float v[2 * NP];
+#pragma unroll
+                        for (int i = 0; i < PP; ++i) {
+                            const Pair qq = q[j0 + j][i], ht = fma2(u, b[j][i], qq);
+                            g[i] = fma2(c[j][i], dd, g[i]);
+                            const Pair gq = mul2(g[i], qq);
+                            y = i ? fma2(ht, c[j][i], y) : mul2(ht, c[j][i]);
+                            gb = i ? fma2(g[i], b[j][i], gb) : mul2(g[i], b[j][i]);
+                            gqa = i ? fma2(gq, A2[i], gqa) : mul2(gq, A2[i]);
+                            dAk[i] = fma2(gq, dl, dAk[i]);
+                            unpair(mul2(g[i], u), v[2 * i], v[2 * i + 1]);
+                            unpair(mul2(ht, dd), v[NP + 2 * i], v[NP + 2 * i + 1]);
+                            g[i] = mul2(a[j0 + j][i], g[i]);
+                        }
+                        float lo, hi;
+                        unpair(y, lo, hi);
+                        sums[0][j] = lo + hi;
+                        unpair(gb, lo, hi);
+                        sums[1][j] = lo + hi;
+                        unpair(gqa, lo, hi);
+                        sums[2][j] = lo + hi;
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) sums[m][j] = set_sum<K>(sums[m][j]);
+                        ChannelSum<K>::run(v, lane);
+#pragma unroll
+                        for (int i = 0; i < ChannelSum<K>::kKept; ++i) dbc[j][i] = v[i];
+                    }
+                    const int ys = y_slot<K>(at.li), vi = ChannelSum<K>::at(lane);
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int t = k * kSub + j0 + j;
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) sm.part[m][t][ys][set_of<K>(tid)] = sums[m][j];
+#pragma unroll
+                        for (int i = 0; i < ChannelSum<K>::kKept; ++i)
+                            sm.dbc[warp][t][(vi + i) / NP][at.n0 + (vi + i) % NP] = dbc[j][i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < PP; ++i) {
+                    float lo, hi;
+                    unpair(dAk[i], lo, hi);
+                    dA[2 * i] += (double)lo;
+                    dA[2 * i + 1] += (double)hi;
                 }
             }
-            store_group<VEC, T, E>(p.dx, o, dx, at.count);
-            store_group<VEC, T, E>(p.ddt, o, ddt, at.count);
-            if (p.z) store_group<VEC, T, E>(p.dz, o, dz, at.count);
-        }
-        if (++since == kFlush) {
-            flush();
-            since = 0;
-        }
-        for (int i = tid; i < TT * 2 * N / 4; i += K::NT) {
-            if (t0 + i / (2 * N / 4) >= e) continue;
-            float4 v = reinterpret_cast<const float4*>(&sm.dbc[0][0][0][0])[i];
+            __syncthreads();
+            if (live) {
+                const long o = (t0 + at.gt) * p.C + at.gc;
+                float dx[E], ddt[E], dz[E];
 #pragma unroll
-            for (int w = 1; w < BwdSmem<K>::WARPS; ++w) {
-                const float4 o = reinterpret_cast<const float4*>(&sm.dbc[w][0][0][0])[i];
-                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                for (int i = 0; i < E; ++i) {
+                    float sum[3];
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) {
+                        const float* l = sm.part[m][at.gt][y_slot<K>(at.gi + i)];
+                        sum[m] = l[0] + l[1];
+                        if (K::YL == 4) sum[m] += l[2] + l[3];
+                    }
+                    const float xv = to_f(x.v[i]), dy = sm.dy[at.gt][at.gi + i];
+                    const float delta = sm.du[at.gt][du_slot<K>(at.gt, at.gi + i)].x;
+                    const float D = p.D && i < at.count ? p.D[at.gc + i] : 0.f;
+                    dx[i] = fmaf(sum[1], delta, D * dy);
+                    ddt[i] = fmaf(sum[1], xv, sum[2] * (1.f / kLog2e)) * sigmoid(to_f(dt.v[i]) + bias[i]);
+                    dz[i] = p.z ? to_f(dout.v[i]) * fmaf(D, xv, sum[0]) * dsilu(to_f(z.v[i])) : 0.f;
+                    if (i < at.count) {
+                        dD[i] = fmaf(dy, xv, dD[i]);
+                        dbias[i] += ddt[i];
+                    }
+                }
+                store_group<VEC, T, E>(p.dx, o, dx, at.count);
+                store_group<VEC, T, E>(p.ddt, o, ddt, at.count);
+                if (p.z) store_group<VEC, T, E>(p.dz, o, dz, at.count);
             }
-            reinterpret_cast<float4*>(p.part_bc + ((long)blockIdx.x * tokens + t0) * 2 * N)[i] = v;
+            if (++since == kFlush) {
+                flush();
+                since = 0;
+            }
+            for (int i = tid; i < TT * 2 * N / 4; i += K::NT) {
+                if (t0 + i / (2 * N / 4) >= e) continue;
+                float4 v = reinterpret_cast<const float4*>(&sm.dbc[0][0][0][0])[i];
+#pragma unroll
+                for (int w = 1; w < BwdSmem<K>::WARPS; ++w) {
+                    const float4 o = reinterpret_cast<const float4*>(&sm.dbc[w][0][0][0])[i];
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+                reinterpret_cast<float4*>(p.part_bc + ((long)blockIdx.x * tokens + t0) * 2 * N)[i] = v;
+            }
         }
+        if (s == first && p.dh0 && at.on) store_pairs(p.dh0 + hrow, g);
+        if (!SPLIT) break;
     }
     flush();
     __syncthreads();
     if (!at.on) return;
-    if (p.dh0) store_pairs(p.dh0 + hrow, g);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) p.part_a[hrow + i] = dA[i];
+    for (int i = 0; i < NP; ++i) p.part_a[((long)row * p.C + at.c) * N + at.n0 + i] = dA[i];
     if (at.n0 == 0) {
         double sum[2] = {0.0, 0.0};
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int m = 0; m < 2; ++m) sum[m] += sm.dd[t][at.li][m];
-        p.part_d[((long)n * 2) * p.C + at.c] = sum[0];
-        p.part_d[((long)n * 2 + 1) * p.C + at.c] = sum[1];
+        p.part_d[((long)row * 2) * p.C + at.c] = sum[0];
+        p.part_d[((long)row * 2 + 1) * p.C + at.c] = sum[1];
     }
 }
 
@@ -734,19 +853,20 @@ sum_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict_
     out[(t * G + g) * N + (i < N ? i : i - N)] = from_f<T>(v);
 }
 
-// dA_log, dD and ddt_bias from the sequences' sums, in a fixed order.
+// dA_log, dD and ddt_bias from the sums of the pieces, or of the sequences (pieces <= 1), in a
+// fixed order.
 __global__ void __launch_bounds__(256)
 sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ part_d, const float* __restrict__ A_log,
-                  float* __restrict__ dA_log, float* __restrict__ dD, float* __restrict__ dbias, const Seqs seq, int C, int N) {
+                  float* __restrict__ dA_log, float* __restrict__ dD, float* __restrict__ dbias, const Seqs seq, int pieces, int C, int N) {
     const long id = (long)blockIdx.x * 256 + threadIdx.x, CN = (long)C * N;
     if (id >= CN + 2 * C) return;
     const long i = id < CN ? id : id - CN;
     const double* part = id < CN ? part_a : part_d;
     const long cols = id < CN ? CN : 2 * C;
     double v = 0.0;
-    for (int n = 0; n < seq.N; ++n) {
+    for (int n = 0; n < (pieces > 1 ? pieces : seq.N); ++n) {
         long s, e;
-        if (seq.bounds(n, s, e)) v += part[(long)n * cols + i];
+        if (pieces > 1 || seq.bounds(n, s, e)) v += part[(long)n * cols + i];
     }
     if (id < CN) dA_log[i] = (float)(v * -(double)expf(A_log[i]));
     else if (i < C) { if (dD) dD[i] = (float)v; }

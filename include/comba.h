@@ -457,7 +457,9 @@ int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, 
  * to every input: dx, ddt, dz, dBm, dCm in the element type, dA_log [C, N], dD [C],
  * ddt_bias [C] and dh0 [nseq, C, N] in fp32.  dz is given exactly when z is; dD, ddt_bias
  * and dh0 may be NULL (skipped), dh_final too (zero).  The states are formed again, from
- * h0; the outputs of the forward are not needed.  dh0 and dh_final 16-byte aligned.
+ * h0 (one for every 8 tokens lies in the workspace); the outputs of the forward are not
+ * needed.  Few long sequences run in pieces, as in the forward.  dh0 and dh_final 16-byte
+ * aligned.
  */
 size_t comba_selective_scan_bwd_workspace_size(int nseq, int T, int C, int G, int N, int packed);
 int comba_selective_scan_bwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,

@@ -219,7 +219,7 @@ def test_scan_in_pieces(lengths, C, G, N, dtype):
     lead = (b[-1],) if packed else (n, lengths[0])
     cu = torch.tensor(b, dtype=torch.int32, device="cuda") if packed else None
     a, kw, v = scan_args(dev(h), lead)
-    ro, rh, _ = scan_reference(h, b, backward=False)
+    ro, rh, rg = scan_reference(h, b)
     out, hf = cdr.selective_scan(*a, **kw, cu_seqlens=cu)
     # twice the roundings of 300 tokens and more of them: sqrt(1600 / 300) times SCAN
     check("out", out.view(-1, C), ro, 3 * SCAN + HALF[dtype])
@@ -227,6 +227,16 @@ def test_scan_in_pieces(lengths, C, G, N, dtype):
     state = kw["h0"].clone()
     out2, _ = cdr.selective_scan(*a, **dict(kw, h0=state), h_final=state, cu_seqlens=cu)
     assert torch.equal(out2, out) and torch.equal(state, hf)
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"], cu_seqlens=cu)
+    for k in IN_KEYS:
+        check("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
+    # without states and gate, and again: the same bits
+    kw = dict(kw, h0=None, z=None)
+    g, g2 = (cdr.selective_scan_bwd(*a, v["dout"], **kw, cu_seqlens=cu) for _ in range(2))
+    assert all(torch.equal(g[k], g2[k]) for k in g if g[k] is not None)
+    _, _, rg = scan_reference(dict(h, h0=None, z=None, dh=None), b)
+    for k in ("x", "dt", "A_log", "Bm", "Cm", "D", "dt_bias"):
+        check("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
     torch.cuda.synchronize()
     assert cdr.get_last_error() == 0
 
@@ -350,6 +360,41 @@ def test_nothing_behind_the_last_sequence_is_touched():
     g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"], cu_seqlens=cu)
     for k in IN_KEYS:
         check("d" + k, g["d" + k][:25] if k in TOKEN_KEYS else g["d" + k], rg[k], SCAN_BWD)
+
+
+def test_malformed_bounds_in_pieces_are_reported():
+    cu = torch.tensor([0, 300, 5000, 800], dtype=torch.int32).cuda()
+    lib, T, C, N = cdr.library(), 1000, 16, 16
+    assert min(lib.comba_selective_scan_fwd_workspace_size(3, T, C, 1, N, 1),
+               lib.comba_selective_scan_bwd_workspace_size(3, T, C, 1, N, 1)) > 0
+    h = scan_inputs(T, 3, C, 1, N, F32, 3, "Dbzh")
+    a, kw, v = scan_args(dev(h))
+    out, _ = cdr.selective_scan(*a, **kw, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == -1
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == -1 and cdr.get_last_error() == 0
+    first = {k: (t[:300] if k in TOKEN_KEYS and t is not None else t) for k, t in h.items()}
+    ro, _, rg = scan_reference(dict(first, dh=None), [0, 300])
+    check("out of the sound sequence", out[:300], ro, SCAN)
+    check("its dx", g["dx"][:300], rg["x"], SCAN_BWD)
+
+
+def test_tokens_without_any_sequence():
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")     # N = 0
+    d = dev(conv_inputs(30, 0, 16, 4, BF, 3, True, True))
+    a, kw, v = scan_args(dev(scan_inputs(30, 0, 16, 1, 16, BF, 3, "Dbzh")))
+    out = torch.full((30, 16), 7.0, dtype=BF, device="cuda")
+    cdr.short_conv(d["x"], d["weight"], d["bias"], d["init"], cu_seqlens=cu, out=out)
+    cdr.selective_scan(*a, **kw, cu_seqlens=cu, out=out)
+    assert bool((out == 7).all())
+    g = cdr.short_conv_bwd(d["x"], d["weight"], d["dout"], d["bias"], d["init"], cu_seqlens=cu)
+    assert bool((g["dweight"] == 0).all()) and bool((g["dbias"] == 0).all())
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, cu_seqlens=cu)
+    assert all(bool((g[k] == 0).all()) for k in ("dA_log", "dD", "ddt_bias"))
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == 0
 
 
 def test_malformed_bounds_are_reported():
