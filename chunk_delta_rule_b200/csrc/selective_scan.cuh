@@ -873,9 +873,9 @@ sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ 
     else if (dbias) dbias[i - C] = (float)v;
 }
 
-// One token: the state h [B, C, N] is read and written once, which bounds it: 34 us for B256
-// C4096 N16, 143 MB at 4.2 TB/s (40 us with one sequence a block).  A block takes kStepSeqs
-// sequences of its channels, all their loads in flight together.
+// One token: the state h [B, C, N] is read and written once, which bounds it: 31 us for B256
+// C4096 N16, 143 MB at 4.6 TB/s.  A block takes kStepSeqs sequences of its channels, all their
+// loads in flight together (2, 4, 8 of them: 33, 31, 35 us; without the streaming hints 35).
 constexpr int kStepSeqs = 4;
 template <typename T, class K>
 __global__ void __launch_bounds__(K::NT)
@@ -887,7 +887,8 @@ step_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int k = 0; k < kStepSeqs; ++k) {
         const long n = first + min(k, count - 1), o = n * p.C + at.c, g = (n * p.G + at.g) * N + at.n0;
-        load_v<4>(p.h_final + o * N + at.n0, h[k]);
+        const float4 hv = __ldcs(reinterpret_cast<const float4*>(p.h_final + o * N + at.n0));   // not read again
+        h[k][0] = hv.x; h[k][1] = hv.y; h[k][2] = hv.z; h[k][3] = hv.w;
         load_v<4>(static_cast<const T*>(p.Bm) + g, b[k]);
         load_v<4>(static_cast<const T*>(p.Cm) + g, c[k]);
         x[k] = to_f(static_cast<const T*>(p.x)[o]);
@@ -912,7 +913,7 @@ step_kernel(const __grid_constant__ Params p) {
             h[k][2 * i + 1] = hi;
             y = fmaf(lo, c[k][2 * i], fmaf(hi, c[k][2 * i + 1], y));
         }
-        if (at.on) store_v<4>(p.h_final + o * N + at.n0, h[k]);
+        if (at.on) __stcs(reinterpret_cast<float4*>(p.h_final + o * N + at.n0), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
 #pragma unroll
         for (int w = 1; w < K::LPC; w *= 2) y += __shfl_xor_sync(0xffffffffu, y, w);
         if (at.on && at.n0 == 0) {
