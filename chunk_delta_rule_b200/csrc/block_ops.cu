@@ -362,11 +362,13 @@ int scan_sums(const scan::Params& p, void* dB, void* dC, float* dA_log, float* d
 #define COMBA_SCAN_DISPATCH(f, dtype, N, ...) \
     ((dtype) == COMBA_BF16 ? COMBA_SCAN_N(f, bf16, N, __VA_ARGS__) : COMBA_SCAN_N(f, float, N, __VA_ARGS__))
 
-// Sizes of a scan: COMBA_OK, or why it is refused.
+// Sizes of a scan: COMBA_OK, or why it is refused.  Without a sequence the groups have to be
+// right all the same: the backward goes on there, to zero the parameters' gradients.
 int scan_sizes(int nseq, int T, int C, int G, int N, int dtype, size_t tokens) {
     if (nseq < 0 || T < 0 || C < 0 || !states_ok(N) || !dtype_ok(dtype)) return COMBA_EINVAL;
-    if (nseq == 0 || C == 0) return COMBA_OK;
+    if (C == 0) return COMBA_OK;
     if (G < 1 || C % G) return COMBA_EINVAL;
+    if (nseq == 0) return COMBA_OK;
     if (volume(tokens, C) > kMaxElements || volume(tokens, G, N) > kMaxElements || volume(nseq, C, N) > kMaxElements)
         return COMBA_EINVAL;
     if (nseq > 65535) return COMBA_EUNSUPPORTED;

@@ -210,3 +210,10 @@ def test_gradients_of_the_definitions():
     assert torch.autograd.gradcheck(ref.gated_norm, (x, g, w))
     x, r, w, sc, po = _doubles((3, 5), (3, 5), (5,), (5,), (5,))
     assert torch.autograd.gradcheck(ref.residual_norm, (x, r, w, sc, po))
+
+
+@pytest.mark.parametrize("G", [0, 3, -1, 64])
+@pytest.mark.parametrize("name,none", [("comba_selective_scan_fwd", dict(n=0)), ("comba_selective_scan_bwd", dict(n=0)),
+                                       ("comba_selective_scan_step", dict(B=0))])
+def test_groups_that_do_not_divide_the_channels_are_refused_without_a_sequence(lib, name, none, G):
+    assert call(lib, name, G=G, **none) == EINVAL
