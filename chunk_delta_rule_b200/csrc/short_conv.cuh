@@ -415,11 +415,12 @@ step_kernel(const T* __restrict__ x, const float* __restrict__ weight, const flo
     const int cv = C / V;
     const long n0 = id / cv * per;
     if (n0 >= B) return;
-    const int c = (int)(id % cv) * V, end = (int)min(n0 + per, (long)B);
+    const int c = (int)(id % cv) * V;
+    const long end = min(n0 + per, (long)B);
     float w[W][V], b[V];
     load_filter<W, V>(weight, bias, c, w, b);
 #pragma unroll 1
-    for (int n = (int)n0; n < end; n += kStepSeqs) {
+    for (long n = n0; n < end; n += kStepSeqs) {   // may pass 2^31 behind the last sequence
         float h[kStepSeqs][W][V];
 #pragma unroll
         for (int k = 0; k < kStepSeqs; ++k) {

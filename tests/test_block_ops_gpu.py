@@ -796,3 +796,31 @@ def test_scan_past_two_to_the_31_elements():
     assert all(bool(torch.isfinite(b[k]).all()) for k in ("dA_log", "ddt_bias"))
     torch.cuda.synchronize()
     assert cdr.get_last_error() == 0
+
+
+# ---------------------------------------------------------------- steps of many sequences
+
+@pytest.mark.parametrize("B,C,W,dtype", [(1301, 936, 4, BF), (1303, 233, 3, F32)])
+def test_conv_step_with_several_sequences_a_thread(B, C, W, dtype):
+    # enough sequences for a thread to take four, and fewer for the last one
+    h = conv_inputs(B, B, C, W, dtype, 41, True, True)
+    d = dev(h)
+    out = cdr.short_conv_step(d["x"], d["weight"], d["init"], d["bias"])
+    ro, rf = ref.short_conv(h["x"], h["weight"], h["bias"], h["init"], list(range(B + 1)))
+    check("out", out, ro, CONV + HALF[dtype])
+    check("state", d["init"], rf, 0.0)
+
+
+def test_conv_step_of_two_to_the_31_sequences():
+    # small whole numbers: every product and sum is exact
+    B = 2 ** 31 - 1
+    x = (torch.arange(B, dtype=torch.int32, device="cuda") % 61).to(BF).view(B, 1)
+    state = (torch.arange(B, dtype=torch.int32, device="cuda") % 59).to(BF).view(B, 1, 1)
+    w = torch.tensor([[1.0, 2.0]], device="cuda")
+    out = cdr.short_conv_step(x, w, state, silu=False)
+    torch.cuda.synchronize()
+    assert torch.equal(state.view(B, 1), x)
+    x.mul_(2)
+    out.sub_(x)             # 2 x + state is at most 178, exact in bf16, and so is the difference
+    assert torch.equal(out.view(B), (torch.arange(B, dtype=torch.int32, device="cuda") % 59).to(BF))
+    assert cdr.get_last_error() == 0
