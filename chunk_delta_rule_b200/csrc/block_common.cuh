@@ -183,7 +183,7 @@ struct Seqs {
         if (!cu) return (int)(t / T);
         int lo = 0, hi = N - 1;
         while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
+            const int mid = hi - ((hi - lo) >> 1);   // the upper middle; lo + hi may pass 2^31
             if (cu[mid] <= t) lo = mid;
             else hi = mid - 1;
         }

@@ -824,3 +824,24 @@ def test_conv_step_of_two_to_the_31_sequences():
     out.sub_(x)             # 2 x + state is at most 178, exact in bf16, and so is the difference
     assert torch.equal(out.view(B), (torch.arange(B, dtype=torch.int32, device="cuda") % 59).to(BF))
     assert cdr.get_last_error() == 0
+
+
+def test_packed_bounds_of_more_than_two_to_the_30_sequences():
+    # nearly all of them empty; the tokens are in the last ones, the search ends behind 2^30
+    N, T = 1_200_000_000, 300
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda").sub_(N - T).clamp_(min=0)
+    cu[N - T + 100:N - T + 150] = 100       # empty ones and one of 50 tokens among those of one token
+    h = conv_inputs(T, 1, 5, 2, F32, 43, True, False)
+    d = dev(h)
+    b = [0, *range(1, 101), *range(150, T + 1)]
+    out, _ = cdr.short_conv(d["x"], d["weight"], d["bias"], cu_seqlens=cu, return_state=False)
+    g = cdr.short_conv_bwd(d["x"], d["weight"], d["dout"], d["bias"], cu_seqlens=cu)
+    x, w, bi = leaf(h["x"]), leaf(h["weight"]), leaf(h["bias"])
+    ro, _ = ref.short_conv(x, w, bi, None, b)
+    rx, rw, rb = grads([ro], [h["dout"]], [x, w, bi])
+    check("out", out, ro, CONV)
+    check("dx", g["dx"], rx, CONV)
+    check("dweight", g["dweight"], rw, CONV)
+    check("dbias", g["dbias"], rb, CONV)
+    torch.cuda.synchronize()
+    assert cdr.get_last_error() == 0
