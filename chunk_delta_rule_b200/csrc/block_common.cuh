@@ -138,8 +138,8 @@ __device__ __forceinline__ float dsilu(float v) {
     return s * (1.f + v * (1.f - s));
 }
 
-// softplus(v) = log(1 + e), e = exp(v); above 20 it is v to fp32 precision, -inf gives 0.
-// The exponent v log2(e) is taken in two parts, since its rounding alone would be 3e-7 of e at
+// softplus(v) = log(1 + e), e = exp(v); above 20 it is v to fp32 precision, -inf gives 0, and
+// NaN stays NaN (a token must not pass for one with dt = -inf).  The exponent v log2(e) is taken in two parts, since its rounding alone would be 3e-7 of e at
 // v = -7, where time steps of 1e-3 lie.  Up to e = 1/2 as 2 atanh(s) with s = e / (2 + e) <=
 // 1/5, by atanh's series up to s^11 (the next term is 6e-10 of the sum), which keeps the
 // relative precision of small results; above, from the hardware's logarithm of 1 + e, whose
@@ -156,7 +156,7 @@ __device__ __forceinline__ float softplus(float v) {
     r = fmaf(q, r, 1.f / 3.f);
     r = 2.f * fmaf(q * s, r, s);
     r = e > 0.5f ? __logf(1.f + e) : r;
-    return v > 20.f ? v : r;
+    return v <= 20.f ? r : v;   // NaN too: fmaxf has dropped it from r
 }
 
 // Sequence bounds on the joint token axis: N uniform sequences of T tokens, or packed

@@ -845,3 +845,47 @@ def test_packed_bounds_of_more_than_two_to_the_30_sequences():
     check("dbias", g["dbias"], rb, CONV)
     torch.cuda.synchronize()
     assert cdr.get_last_error() == 0
+
+
+# ---------------------------------------------------------------- NaN, and decays past fp32
+
+def same_where_finite(name, got, want, tol):
+    """NaN exactly where the definition has NaN, and its values elsewhere."""
+    got, want = got.detach().double().cpu(), want.detach().double().cpu()
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    assert torch.equal(got.isnan(), want.isnan()), f"{name}: NaN in {int(got.isnan().sum())} places, {int(want.isnan().sum())} expected"
+    check(name, got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0), tol)
+
+
+@pytest.mark.parametrize("where", ["dt", "dt_bias"])
+@pytest.mark.parametrize("T,C,N,dtype", [(50, 5, 16, F32), (50, 8, 8, BF), (37, 5, 128, F32), (1000, 33, 16, F32)])
+def test_a_nan_time_step_stays_one(T, C, N, dtype, where):
+    # as in the definition: its channel's outputs and state from that token on, and the
+    # gradients that they enter; 1000 tokens run in pieces
+    lib = cdr.library()
+    assert (lib.comba_selective_scan_fwd_workspace_size(1, T, C, 1, N, 0) > 0) == (T == 1000)
+    assert lib.comba_selective_scan_bwd_workspace_size(1, T, C, 1, N, 0) > 0
+    h = scan_inputs(T, 1, C, 1, N, dtype, 31, "Dbzh")
+    h["dt_bias"] -= 2
+    if where == "dt":
+        h["dt"][2 * T // 5, 3] = float("nan")
+    else:
+        h["dt_bias"][3] = float("nan")
+    a, kw, v = scan_args(dev(h), (1, T))
+    out, hf = cdr.selective_scan(*a, **kw)
+    ro, rh, rg = scan_reference(h, [0, T])
+    assert bool(ro.isnan().any()) and not bool(ro.isnan().all())
+    tol = 3 * SCAN + HALF[dtype]      # as for 1600 tokens in pieces
+    same_where_finite("out", out[0], ro, tol)
+    same_where_finite("h_final", hf, rh, tol)
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"])
+    for k in IN_KEYS:
+        same_where_finite("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
+    # one token of two sequences, the second one without it
+    one = {k: (torch.cat([t[2 * T // 5][None], t[:1]]) if k in TOKEN_KEYS else t) for k, t in h.items()}
+    one["h0"] = torch.cat([h["h0"], h["h0"]])
+    o = dev(one)
+    out = cdr.selective_scan_step(o["x"], o["dt"], o["A_log"], o["Bm"], o["Cm"], o["h0"], D=o["D"], dt_bias=o["dt_bias"], z=o["z"])
+    ro, rh, _ = scan_reference(one, [0, 1, 2], backward=False)
+    same_where_finite("step", out, ro, SCAN + HALF[dtype])
+    same_where_finite("state", o["h0"], rh, SCAN)
