@@ -9,6 +9,8 @@
 // neighbouring lanes hold a channel.
 #pragma once
 
+#include <float.h>
+
 #include "block_common.cuh"
 
 namespace comba {
@@ -314,12 +316,19 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Plac
     }
 }
 
+// A log2(e), down to the lowest finite float: there every delta > 0 that counts gives a decay of
+// 0 all the same, and delta = 0 (dt = -inf, tokens past the end) one of 1 instead of 0 * inf.
 template <class K>
 __device__ __forceinline__ void load_decays(const Params& p, const Place<K>& at, Pair (&A2)[K::PP]) {
     float a[K::NP];
     load_v<K::NP>(p.A_log + (long)at.c * K::N + at.n0, a);
 #pragma unroll
-    for (int i = 0; i < K::PP; ++i) A2[i] = pair(-expf(a[2 * i]) * kLog2e, -expf(a[2 * i + 1]) * kLog2e);
+    for (int i = 0; i < K::NP; ++i) {
+        a[i] = -expf(a[i]) * kLog2e;
+        a[i] = a[i] < -FLT_MAX ? -FLT_MAX : a[i];   // NaN stays
+    }
+#pragma unroll
+    for (int i = 0; i < K::PP; ++i) A2[i] = pair(a[2 * i], a[2 * i + 1]);
 }
 
 // One block per (channel block, sequence).
@@ -868,7 +877,7 @@ sum_params_kernel(const double* __restrict__ part_a, const double* __restrict__ 
         long s, e;
         if (pieces > 1 || seq.bounds(n, s, e)) v += part[(long)n * cols + i];
     }
-    if (id < CN) dA_log[i] = (float)(v * -(double)expf(A_log[i]));
+    if (id < CN) dA_log[i] = (float)(v * -exp((double)A_log[i]));   // in double: v is 0 where fp32's A overflows
     else if (i < C) { if (dD) dD[i] = (float)v; }
     else if (dbias) dbias[i - C] = (float)v;
 }

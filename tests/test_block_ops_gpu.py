@@ -889,3 +889,29 @@ def test_a_nan_time_step_stays_one(T, C, N, dtype, where):
     ro, rh, _ = scan_reference(one, [0, 1, 2], backward=False)
     same_where_finite("step", out, ro, SCAN + HALF[dtype])
     same_where_finite("state", o["h0"], rh, SCAN)
+
+
+@pytest.mark.parametrize("T,N,dtype", [(16, 16, F32), (21, 16, F32), (21, 8, BF), (9, 64, F32), (1003, 16, F32)])
+def test_decay_rates_past_the_largest_float(T, N, dtype):
+    # exp(100) is infinite in fp32: such an entry forgets at once, whatever the length, but
+    # for tokens with delta = 0, which leave it as it is
+    C = 12
+    h = scan_inputs(T, 1, C, 1, N, dtype, 17, "Dbzh")
+    h["A_log"][:4] = 100.0
+    a, kw, v = scan_args(dev(h), (1, T))
+    out, hf = cdr.selective_scan(*a, **kw)
+    ro, rh, rg = scan_reference(h, [0, T])
+    assert all(bool(torch.isfinite(t).all()) for t in (ro, rh, *rg.values()))
+    check("out", out[0], ro, 3 * SCAN + HALF[dtype])
+    check("h_final", hf, rh, 3 * SCAN)
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"])
+    for k in IN_KEYS:
+        check("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
+    h["A_log"][:2] = float("inf")
+    h["dt"][T // 2:, 2:4] = -float("inf")
+    a, kw, v = scan_args(dev(h), (1, T))
+    out, hf = cdr.selective_scan(*a, **kw)
+    ro, rh, _ = scan_reference(h, [0, T], backward=False)
+    assert bool(torch.isfinite(rh).all())
+    check("out", out[0], ro, 3 * SCAN + HALF[dtype])
+    check("h_final", hf, rh, 3 * SCAN)
