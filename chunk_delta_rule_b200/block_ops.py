@@ -102,11 +102,19 @@ class _Call:
             raise _cdr.CombaError(st, name)
 
 
+_INT_MAX = 0x7FFFFFFF
+
+
+def _ints(name: str, *sizes: int) -> None:
+    """Refuses sizes that the C ABI's ints cannot hold (ctypes would cut them)."""
+    if max(sizes, default=0) > _INT_MAX:
+        raise ValueError(f"{name} must have dimensions below 2^31 (got {sizes})")
+
+
 def _tokens(x, cu_seqlens, name: str = "x"):
     """(leading shape, N, T, C) of a token tensor: N sequences of T tokens, or T packed."""
     _element(x, name)
-    if max(x.shape, default=0) > 0x7FFFFFFF:
-        raise ValueError(f"{name} must have dimensions below 2^31 (got {tuple(x.shape)})")
+    _ints(name, *x.shape)
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError(f"{name} must be [B, T, C]")
@@ -115,6 +123,7 @@ def _tokens(x, cu_seqlens, name: str = "x"):
         raise ValueError(f"{name} must be [total_T, C] with cu_seqlens")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [N + 1]")
+    _ints("cu_seqlens", cu_seqlens.numel() - 1)
     return (x.shape[0],), cu_seqlens.numel() - 1, x.shape[0], x.shape[1]
 
 
@@ -122,6 +131,7 @@ def _filter(weight, C: int, dev):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [C, W]")
     W = weight.shape[1]
+    _ints("weight", W)
     _tensor(weight, "weight", _F32, (C, W), dev)
     return W
 
@@ -190,6 +200,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
+    _ints("x", B, C)
     dev = _device(x, "x")
     _tensor(x, "x", dt, (B, C), dev)
     W = _filter(weight, C, dev)
@@ -203,6 +214,12 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     return out
 
 
+def _groups_states(Bm):
+    G, N = Bm.shape[-2:]
+    _ints("Bm", G, N)
+    return G, N
+
+
 def _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z):
     """(groups, states) of a scan whose token tensors have the leading shape ``lead``."""
     et, dev, shape = x.dtype, _device(x, "x"), x.shape
@@ -210,7 +227,7 @@ def _scan_inputs(lead, C, x, dt, A_log, Bm, Cm, D, dt_bias, z):
     _tensor(dt, "dt", et, shape, dev)
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
         raise ValueError("Bm must be [..., G, N]")
-    G, N = Bm.shape[-2:]
+    G, N = _groups_states(Bm)
     _tensor(A_log, "A_log", _F32, (C, N), dev)
     _tensor(Bm, "Bm", et, (*lead, G, N), dev)
     _tensor(Cm, "Cm", et, (*lead, G, N), dev)
@@ -296,6 +313,7 @@ def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
+    _ints("x", B, C)
     dev = _device(x, "x")
     G, N = _scan_inputs((B,), C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
     _tensor(h, "h", _F32, (B, C, N), dev)
@@ -312,6 +330,7 @@ def _norm_rows(x, name: str = "x"):
     if x.dim() < 1:
         raise ValueError(f"{name} must be [..., D]")
     D = x.shape[-1]
+    _ints(name, D)
     return dt, D, (x.numel() // D if D else 0)
 
 

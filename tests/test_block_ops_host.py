@@ -217,3 +217,21 @@ def test_gradients_of_the_definitions():
                                        ("comba_selective_scan_step", dict(B=0))])
 def test_groups_that_do_not_divide_the_channels_are_refused_without_a_sequence(lib, name, none, G):
     assert call(lib, name, G=G, **none) == EINVAL
+
+
+@pytest.mark.parametrize("wide", [2 ** 31, 2 ** 32 + 4])
+def test_the_binding_refuses_dimensions_past_an_int(wide):
+    # the C ABI takes them as int: what is wider must not arrive cut to its low 32 bits
+    t = lambda *s: torch.zeros((1,) * len(s)).expand(s)     # no memory behind them
+    w = torch.zeros(8, 4)
+    a = torch.zeros(2, 8)
+    for f in (lambda: cdr.short_conv(t(2, wide, 8), w), lambda: cdr.short_conv(t(2, 5, wide), w),
+              lambda: cdr.short_conv_step(t(wide, 8), w, a), lambda: cdr.short_conv_step(t(2, wide), w, a),
+              lambda: cdr.selective_scan_step(t(wide, 8), a, a, a, a, a), lambda: cdr.selective_scan_step(t(2, wide), a, a, a, a, a),
+              lambda: cdr.gated_norm(t(3, wide), a, w), lambda: cdr.gated_norm_bwd(t(wide), a, w, a),
+              lambda: cdr.residual_norm(t(3, wide), a, w), lambda: cdr.residual_norm_bwd(t(3, wide), a, w, a),
+              lambda: cdr.short_conv(t(5, 8), w, cu_seqlens=t(wide + 1)),
+              lambda: cdr.block_ops._filter(t(8, wide), 8, 0),
+              lambda: cdr.block_ops._groups_states(t(2, wide, 16)), lambda: cdr.block_ops._groups_states(t(2, 1, wide))):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            f()
