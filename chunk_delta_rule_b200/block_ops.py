@@ -106,7 +106,8 @@ _INT_MAX = 0x7FFFFFFF
 
 
 def _ints(name: str, *sizes: int) -> None:
-    """Refuses sizes that the C ABI's ints cannot hold (ctypes would cut them)."""
+    """Refuses sizes that the C ABI's ints cannot hold (ctypes would cut them).  A decode
+    step asks only once a comparison has found one: a call here is 0.35 us."""
     if max(sizes, default=0) > _INT_MAX:
         raise ValueError(f"{name} must have dimensions below 2^31 (got {sizes})")
 
@@ -131,7 +132,8 @@ def _filter(weight, C: int, dev):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [C, W]")
     W = weight.shape[1]
-    _ints("weight", W)
+    if W > _INT_MAX:
+        _ints("weight", W)
     _tensor(weight, "weight", _F32, (C, W), dev)
     return W
 
@@ -200,7 +202,8 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
-    _ints("x", B, C)
+    if B > _INT_MAX or C > _INT_MAX:
+        _ints("x", B, C)
     dev = _device(x, "x")
     _tensor(x, "x", dt, (B, C), dev)
     W = _filter(weight, C, dev)
@@ -216,7 +219,8 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
 
 def _groups_states(Bm):
     G, N = Bm.shape[-2:]
-    _ints("Bm", G, N)
+    if G > _INT_MAX or N > _INT_MAX:
+        _ints("Bm", G, N)
     return G, N
 
 
@@ -313,7 +317,8 @@ def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, 
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     B, C = x.shape
-    _ints("x", B, C)
+    if B > _INT_MAX or C > _INT_MAX:
+        _ints("x", B, C)
     dev = _device(x, "x")
     G, N = _scan_inputs((B,), C, x, dt, A_log, Bm, Cm, D, dt_bias, z)
     _tensor(h, "h", _F32, (B, C, N), dev)
@@ -330,7 +335,8 @@ def _norm_rows(x, name: str = "x"):
     if x.dim() < 1:
         raise ValueError(f"{name} must be [..., D]")
     D = x.shape[-1]
-    _ints(name, D)
+    if D > _INT_MAX:
+        _ints(name, D)
     return dt, D, (x.numel() // D if D else 0)
 
 
