@@ -219,26 +219,36 @@ bool scan_vector(int C, int G, int dtype, std::initializer_list<const void*> ptr
 int group_blocks(int C, int G, int N) { return (int)ceil_div(C / G, 4 * scan::Layout<16>::NT / N); }
 
 // Pieces of the split form, 1 for the direct one, from the clocks that 16 tokens of a channel
-// block cost.  A packed batch's longest sequence is taken to be 4 times the mean.  Measured at
-// C2048 N16, direct and split, forward: T4096 of 1 sequence 328 and 130 us, of 2 329 and 241, of 3
-// 382 and 350, of 4 383 and 459; T512 46 and 34; T16384 C64 1286 and 44; T300 C256 29 and 33.
-// Backward: T4096 of 1 1030 and 557, of 2 1038 and 1073, of 3 1291 and 1565; T512 145 and 98;
-// T4096 C256 997 and 98.
+// block cost: the direct form takes as long as its longest sequence, or as all of them on all
+// SMs; the split form as one piece, with an SM's other blocks beside it.  Measured at C2048 N16,
+// direct and split, forward: T4096 of 1 sequence 322 and 135 us, of 2 322 and 250, of 3 369 and
+// 363, of 4 369 and 473; T512 47 and 35; T16384 C64 1257 and 45; T300 C256 29 and 35; T2048 C2048
+// N32 162 and 131.  Backward: T4096 of 1 1032 and 561, of 2 1036 and 1079, of 3 1291 and 1568;
+// T4096 C1024 of 2 1033 and 516, of 4 1063 and 968, of 6 1299 and 1428; T512 of 1 146 and 98, of
+// 2 147 and 164; T4096 C256 1022 and 102; T2048 of 1, C1024 N64 561 and 470, C768 N32 496 and
+// 195, C512 N128 514 and 604, C2048 N8 770 and 221.
+//
+// The lengths of a packed batch are not known here.  Its longest sequence is taken to be 4 times
+// the mean, between the two ways to be wrong (direct and split, forward / backward): 8 equal
+// sequences of 1024, C1024, run in pieces, 98 and 135 / 348 and 490 us; one of 8192 and 32 of
+// 128, C2048, run direct, 658 and 344 / 2137 and 1598 us.
 struct SplitCosts {
     double lone, shared, more;   // clocks: alone on an SM, in a full one, the split form's sweeps
     int blocks;                  // that an SM holds
 };
-constexpr SplitCosts kFwdCosts{2950, 1290, 700, 4}, kBwdCosts{7600, 4700, 1500, 2};
+constexpr SplitCosts kFwdCosts{2950, 1290, 700, 4};
+constexpr SplitCosts bwd_costs(int N) { return N == 64 ? SplitCosts{8300, 4700, 2300, 2} : SplitCosts{7600, 4700, 3550, 2}; }
 int scan_pieces(const Seqs& q, int C, int G, int N, const SplitCosts& k) {
     if (q.tokens() <= 0) return 1;
     const double sm_blocks = (double)G * group_blocks(C, G, N) / kSMs;
     const double tiles = q.tokens() / 16.0, mean = tiles / q.N;
     const double longest = q.cu ? (4 * mean < tiles ? 4 * mean : tiles) : mean;
-    const double direct = std::max(longest * k.lone, tiles * sm_blocks * k.shared), split = tiles * sm_blocks * (k.shared + k.more);
     const long most = std::min<long>(128, q.tokens() / 128);
-    const long fit = (long)(k.blocks / sm_blocks);   // one wave of blocks
-    const long pieces = std::min(most, fit);
-    return pieces >= 2 && split * std::max(1.0, fit / (double)pieces) < direct ? (int)pieces : 1;
+    const long pieces = std::min(most, (long)(k.blocks / sm_blocks));   // in one wave of blocks
+    if (pieces < 2) return 1;
+    const double direct = std::max(longest * k.lone, tiles * sm_blocks * k.shared);
+    const double split = tiles / pieces * k.blocks * (k.shared + k.more);
+    return split < direct ? (int)pieces : 1;
 }
 
 // Pieces of whole tiles; they may come out fewer than wanted.
@@ -278,7 +288,7 @@ ScanWs scan_ws(const Seqs& q, int C, int G, int N) {
     ScanWs w{};
     size_t o = 0;
     auto take = [&](size_t n) { const size_t at = o; o += (n + 255) & ~(size_t)255; return at; };
-    cut(q, scan_pieces(q, C, G, N, kBwdCosts), w.piece, w.pieces);
+    cut(q, scan_pieces(q, C, G, N, bwd_costs(N)), w.piece, w.pieces);
     const size_t rows = w.pieces > 1 ? w.pieces : q.N;
     w.ckpt = take((size_t)scan::ckpt_slots(q, w.pieces) * C * N * 4);
     w.bc = take((size_t)G * group_blocks(C, G, N) * q.tokens() * 2 * N * 4);

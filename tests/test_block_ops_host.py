@@ -235,3 +235,34 @@ def test_the_binding_refuses_dimensions_past_an_int(wide):
               lambda: cdr.block_ops._groups_states(t(2, wide, 16)), lambda: cdr.block_ops._groups_states(t(2, 1, wide))):
         with pytest.raises(ValueError, match=r"2\^31"):
             f()
+
+
+# Sizes (sequences, T, C, N) with the measured times (us) of the scan's direct and split forms,
+# forward and backward.
+SCAN_FORMS = [
+    ((1, 4096, 2048, 16), (322, 135), (1032, 561)), ((2, 4096, 2048, 16), (322, 250), (1036, 1079)),
+    ((3, 4096, 2048, 16), (369, 363), (1291, 1568)), ((4, 4096, 2048, 16), (369, 473), (1303, 1340)),
+    ((1, 512, 2048, 16), (47, 35), (146, 98)), ((2, 512, 2048, 16), (47, 43), (147, 164)),
+    ((2, 1024, 2048, 16), (86, 74), (278, 297)), ((1, 16384, 64, 16), (1257, 45), (4059, 125)),
+    ((2, 4096, 1024, 16), (322, 137), (1033, 516)), ((4, 4096, 1024, 16), (322, 250), (1063, 968)),
+    ((6, 4096, 1024, 16), (369, 363), (1299, 1428)), ((1, 4096, 256, 16), (319, 37), (1022, 102)),
+    ((16, 4096, 256, 16), (320, 244), (1068, 965)), ((3, 4096, 1920, 16), (365, 358), (1289, 1557)),
+    ((1, 2048, 2048, 8), (256, 57), (770, 221)), ((1, 2048, 768, 32), (162, 60), (496, 195)),
+    ((4, 2048, 768, 32), (190, 184), (627, 694)), ((1, 2048, 1024, 64), (133, 125), (561, 470)),
+    ((2, 2048, 512, 64), (133, 127), (558, 475)), ((1, 2048, 512, 128), None, (514, 604)),
+    ((1, 2048, 256, 128), (131, 80), (483, 324)),
+]
+
+
+@pytest.mark.parametrize("size,fwd,bwd", SCAN_FORMS, ids=lambda v: str(v))
+def test_the_scan_takes_the_form_measured_to_be_faster(lib, size, fwd, bwd):
+    n, T, C, N = size
+    if fwd:
+        split = lib.comba_selective_scan_fwd_workspace_size(n, T, C, 1, N, 0) > 0
+        assert split == (fwd[1] < fwd[0])
+    # the backward's workspace in the direct form: states, dB and dC of a channel block of
+    # 512 / N channels, and one row of the parameters' sums for each sequence
+    up = lambda v: -(-v // 256) * 256
+    direct = (up((n * T // 8 + n + 2) * C * N * 4) + up(-(-C * N // 512) * n * T * 2 * N * 4) + up(n * C * N * 8) + up(n * 2 * C * 8))
+    got = lib.comba_selective_scan_bwd_workspace_size(n, T, C, 1, N, 0)
+    assert (got != direct) == (bwd[1] < bwd[0])
