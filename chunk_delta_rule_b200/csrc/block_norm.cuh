@@ -7,11 +7,15 @@
 // read and written once and its statistics are two sums, so the kernels are bound by HBM
 // bandwidth.  A row lies in the registers of the 8 .. 1024 threads that share it, 8 values
 // each: 8 consecutive ones where the rows allow 16-byte accesses, else every TPR-th one,
-// so that any width up to 8192 runs.
+// so that any width up to 8192 runs.  Parameter gradients are summed in fp32 over a thread's
+// rows (111 of 32K rows of 2048), then over the blocks in fp64.
 //
 // Measured, of a copy's 6.55 TB/s: gated norm of 512K bf16 rows of 128, forward 74 us (5.5 TB/s),
 // backward 125 us (5.4); residual norm of 32K rows of 2048, bf16 onto an fp32 stream with
-// post norm, forward 136 us (5.9), backward 219 us (5.5).
+// post norm, forward 136 us (5.9), backward 219 us (5.5).  Above a width of 4096 a block has 1024
+// threads of 64 registers, and the backwards spill: 64M values of width 5120 and 8192, the same,
+// 753 and 547 us (1.6 and 2.2 TB/s), gated 326 and 234 (2.1 and 2.9); fp32 rows onto fp32 at 2048:
+// forward 246 us (4.4, spills too), backward 262 (6.1).
 #pragma once
 
 #include <type_traits>
@@ -26,7 +30,8 @@ using namespace blk;
 constexpr int kMaxWidth = 8192;
 // Blocks of 256 threads of the backwards that an SM's registers hold: 80 registers a thread,
 // and 128 where three column sums and up to four rows are kept (gated with 2, 3, 4 blocks: 152,
-// 126, 165 us; residual with 2, 3: 219, 441 us, the latter for its spills).
+// 126, 165 us in bf16, fp32 rows of 2048 with 3: 264 us, 5.1 TB/s, spilling 72 bytes a thread;
+// residual with 2, 3: 219, 441 us, the latter for its spills).
 constexpr int kGatedBlocks = 3, kResidualBlocks = 2;
 
 // 8 values of a row as they are stored.

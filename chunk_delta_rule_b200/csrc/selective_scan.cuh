@@ -440,10 +440,13 @@ split_kernel(const __grid_constant__ Params p) {
 //   dx = du delta + D dy,  ddt = ddelta sigmoid(dt + dt_bias),  g <- a g.
 // y, du and ddelta's first part are summed over a channel's lanes by the preparers.  dB and
 // dC are summed over a warp's channels by halving shuffles, over the block's warps through
-// shared memory, and leave one row per channel block.
+// shared memory, and leave one row per channel block: 2 N values for 512 / N channels, C N^2 / 64
+// bytes a token to write and read again (B8 T2048 C1024, N = 16, 32, 64, 128: 661 us, 1.17, 2.65,
+// 6.43 ms).
 //
-// What bounds it: the issue slots of the 8 warps an SM's registers hold, 115 instructions for
-// a token of 8 channels.  Measured with the sweep that stores the states: 661 us for B8 T2048
+// What bounds it: latency, with the 8 warps that an SM's registers hold at 248 a thread; the
+// issue slots are 47 % busy with 115 instructions for a token of 8 channels, 28 of which sum dB
+// and dC over the channels.  Measured with the sweep that stores the states: 661 us for B8 T2048
 // C1024 N16 (bf16), 1.24 ms for C2048.  Storing a state every kSub = 8 tokens costs 8 bytes a
 // (token, channel) each way, and spares a third sweep's exponentials.
 constexpr int kFlush = 16;

@@ -8,8 +8,9 @@
 // keeps the filter and the last W-1 inputs of 4 neighbouring channels in registers and
 // walks a tile of tokens (8 channels would take twice the registers, and halve the threads).
 // Measured on B8 T4096 C6144 W4 bf16: forward 133 us, 6.05 TB/s of a copy's 6.55; backward
-// 249 us, 4.85 TB/s, where the issue slots bound it (64 % busy with 16 warps an SM, which
-// the 72 values a thread keeps for its 4 channels' filter, sums and open rows allow).
+// 249 us, 4.85 TB/s, where latency bounds it: neither the issue slots (63 % busy) nor HBM are
+// full with the 16 warps an SM that the 72 values a thread keeps for its 4 channels' filter,
+// sums and open rows allow.
 #pragma once
 
 #include <limits.h>
@@ -405,7 +406,7 @@ sum_kernel(const float* __restrict__ part, float* __restrict__ dweight, float* _
 
 // One token: out = silu(bias + sum_j w_j [state, x]_j), and the state moves on by x.  A thread
 // takes `per` sequences of its channels, kStepSeqs of them in flight, for one load of the
-// filter.
+// filter; with per = 1 (B256 C4096 and fewer) it reads its one sequence's rows kStepSeqs times.
 constexpr int kStepSeqs = 4;
 template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads)

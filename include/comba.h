@@ -377,7 +377,10 @@ int comba_state_compose(const float* RM, const float* S0, float* S_start, int B,
  *    are fp32 or wider; bf16 outputs (gradients of bf16 inputs among them) are rounded
  *    once, to nearest even.
  *  - Channels are the last, contiguous dimension of token tensors: [B, T, C].  Any C is
- *    accepted; multiples of 8 with 16-byte aligned pointers use vector accesses.
+ *    accepted.  Vector accesses need: the convolution C a multiple of 4 and its tensors
+ *    aligned to 4 elements, weight and bias to 16 bytes; the scan C / G a multiple of 4 and
+ *    its token tensors aligned to 4 elements; the norms D a multiple of 8 and 16-byte
+ *    alignment of all tensors.
  *  - `void*` tensors need the alignment of their element, fp32 ones 4 bytes, unless
  *    stated otherwise.
  *  - Sequences: cu_seqlens == NULL means `nseq` sequences of T tokens ([nseq, T, ...]).
@@ -435,12 +438,13 @@ int comba_short_conv_step(const void* x, const float* weight, const float* bias,
  *     h_t[c, n] = exp(delta_t[c] A[c, n]) h_{t-1}[c, n] + delta_t[c] x_t[c] B_t[g(c), n]
  *     y_t[c] = sum_n h_t[c, n] C_t[g(c), n] + D[c] x_t[c],     out_t = y_t silu(z_t)
  * (the discretisation of comba_chunk_fwd_gated, per channel and entry).  dt = -inf makes
- * a token leave the state as it is.
+ * a token leave the state as it is, where its x and B are finite.  A NaN in dt or dt_bias
+ * stays NaN.  Where A overflows fp32 the entry forgets at every token with delta > 0.
  *
  * x, dt, z, out: token tensors of C channels (z NULL: out = y).  Bm, Cm: [tokens, G, N].
  * A_log [C, N], D [C] or NULL (zero), dt_bias [C] or NULL (zero), h0 and h_final
  * [nseq, C, N]: fp32 (h0 NULL: zero; h_final NULL: not written; h_final may be h0 itself,
- * but overlap it in no other way).  G must divide C; N in {8, 16, 32, 64, 128}.  A_log,
+ * but overlap it in no other way).  G must divide C (also without sequences); N in {8, 16, 32, 64, 128}.  A_log,
  * Bm, Cm, h0 and h_final 16-byte aligned.  nseq <= 65535 (COMBA_EUNSUPPORTED above).
  * The workspace may be of size 0 (and NULL): it is for the split form, which cuts few long
  * sequences into pieces and joins them by their state transitions; equal up to rounding.
@@ -459,7 +463,9 @@ int comba_selective_scan_fwd(const void* x, const void* dt, const float* A_log, 
  * and dh0 may be NULL (skipped), dh_final too (zero).  The states are formed again, from
  * h0 (one for every 8 tokens lies in the workspace); the outputs of the forward are not
  * needed.  Few long sequences run in pieces, as in the forward.  dh0 and dh_final 16-byte
- * aligned.
+ * aligned.  The workspace also holds partial sums of dB and dC, 2 N fp32 values a token for
+ * every 512 / N channels, C N^2 / 64 bytes a token, half of it at N = 32 and more above: 0.31,
+ * 0.75, 2.0, 6.0 and 20 GiB in all for 32K tokens of C = 2048 at N = 8, 16, 32, 64 and 128.
  */
 size_t comba_selective_scan_bwd_workspace_size(int nseq, int T, int C, int G, int N, int packed);
 int comba_selective_scan_bwd(const void* x, const void* dt, const float* A_log, const void* Bm, const void* Cm,
