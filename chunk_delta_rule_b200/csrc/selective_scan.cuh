@@ -316,8 +316,9 @@ __device__ __forceinline__ void walk(const Params& p, FwdSmem<K>& sm, const Plac
     }
 }
 
-// A log2(e), down to the lowest finite float: there every delta > 0 that counts gives a decay of
-// 0 all the same, and delta = 0 (dt = -inf, tokens past the end) one of 1 instead of 0 * inf.
+// A log2(e), and -1e30 where that overflows: every delta from 1.5e-28 on gives a decay of 0 all
+// the same, delta = 0 (dt = -inf, tokens past the end) one of 1 instead of 0 * inf, and at those
+// tokens the backward's sum of g q A, which their sigmoid of 0 takes away, stays finite.
 template <class K>
 __device__ __forceinline__ void load_decays(const Params& p, const Place<K>& at, Pair (&A2)[K::PP]) {
     float a[K::NP];
@@ -325,7 +326,7 @@ __device__ __forceinline__ void load_decays(const Params& p, const Place<K>& at,
 #pragma unroll
     for (int i = 0; i < K::NP; ++i) {
         a[i] = -expf(a[i]) * kLog2e;
-        a[i] = a[i] < -FLT_MAX ? -FLT_MAX : a[i];   // NaN stays
+        a[i] = a[i] < -FLT_MAX ? -1e30f : a[i];   // NaN stays
     }
 #pragma unroll
     for (int i = 0; i < K::PP; ++i) A2[i] = pair(a[2 * i], a[2 * i + 1]);

@@ -907,8 +907,15 @@ def test_decay_rates_past_the_largest_float(T, N, dtype):
     g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"])
     for k in IN_KEYS:
         check("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
-    h["A_log"][:2] = float("inf")
+    # with tokens that leave the state as it is: their own gradients vanish
     h["dt"][T // 2:, 2:4] = -float("inf")
+    h["h0"] *= 100
+    a, kw, v = scan_args(dev(h), (1, T))
+    _, _, rg = scan_reference(h, [0, T])
+    g = cdr.selective_scan_bwd(*a, v["dout"], **kw, dh_final=v["dh"])
+    for k in IN_KEYS:
+        check("d" + k, g["d" + k].view(h[k].shape), rg[k], 3 * SCAN_BWD + (HALF[dtype] if k in TOKEN_KEYS else 0.0))
+    h["A_log"][:2] = float("inf")
     a, kw, v = scan_args(dev(h), (1, T))
     out, hf = cdr.selective_scan(*a, **kw)
     ro, rh, _ = scan_reference(h, [0, T], backward=False)
